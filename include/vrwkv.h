@@ -14,6 +14,9 @@
  *   - the Bi-WKV backward pass: the pages state that one exists (in an
  *     appendix they do not reproduce), so vrwkv_biwkv_bwd computes the plain
  *     derivatives of eq. 5.
+ * Beside them stand multi-head decay attention (vrwkv_decay_attn_*: sequences
+ * that grow token by token) and LayerNorm with its gradient
+ * (vrwkv_layer_norm_*), which the pages do not define.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -33,7 +36,8 @@
  *   synchronises.  vrwkv_spatial_gate (and its _ws variant),
  *   vrwkv_channel_mix, vrwkv_spatial_mix_block and vrwkv_biwkv_bwd enqueue
  *   kernel launches only and are replayed from CUDA graphs by the benchmark;
- *   capture of the other calls has not been tested.
+ *   vrwkv_decay_attn_* and vrwkv_layer_norm_* do so too and are replayed from
+ *   CUDA graphs by the tests; capture of the other calls has not been tested.
  * Dtypes.  VRWKV_F32 or VRWKV_BF16 select the storage type of the token
  *   tensors (inputs and output alike).  Arithmetic is float32 throughout;
  *   bfloat16 outputs are rounded to nearest even once, at the store.
@@ -433,6 +437,156 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
                                void* stream);
 
 /*
+ * Multi-head decay attention: causal linear attention with a matrix state per
+ * head that decays at a fixed rate, the counterpart of Bi-WKV (whose decay is
+ * per channel, over a whole image) for sequences that grow token by token.
+ * The pages have no counterpart; these are its formulas.  The C = H*D
+ * channels are H heads of D; per sequence b and head h, with S_{-1} the given
+ * state (zeros by default):
+ *   S_t   = e^{-w_h} S_{t-1} + k_t^T v_t          (D x D; row: k, column: v)
+ *   out_t = scale * q_t S_t
+ *         = scale * [ sum_{s<=t} e^{-w_h (t-s)} (q_t . k_s) v_s
+ *                     + e^{-w_h (t+1)} q_t S_{-1} ]
+ *
+ * Conventions of the three entry points, where they differ from the others'
+ *   q, k, v (and gy)  (B, T, H*D) tensors, dtype `dtype`, whose rows lie ldq,
+ *            ldk, ldv (ldg) >= H*D elements apart, sequences T rows apart: one
+ *            (B, T, 3*H*D) projection's three column slices are such tensors.
+ *            Outputs are dense (B, T, H*D).
+ *   w        float32[H], the decay per token.  w >= 0 in use; a negative w is
+ *            computed as written and grows without bound.  w is a constant of
+ *            the head: no gradient of it is formed.
+ *   states   float32 (B, H, D, D), also for bfloat16 tensors.
+ *   lengths  int32[B] in device memory, or NULL (every sequence has T tokens).
+ *            Sequence b's tokens are its first lengths[b] (values are taken
+ *            into [0, T]); later rows of the inputs are not used, whatever
+ *            they hold, later rows of the outputs are zeros, and its final
+ *            state is the one after its last token (the given one if it has
+ *            none).
+ *   workspace  device memory of at least vrwkv_decay_attn_workspace_bytes(B,
+ *            T, H, D, dtype, backward) bytes, 256-byte aligned (NULL if that
+ *            is 0): the states at the cuts of long sequences.  Its contents
+ *            need no preparation.  Calls that may run at the same time need
+ *            separate workspaces.
+ * Limits: D <= 128 (UNSUPPORTED above).
+ * Arithmetic: products, sums and states in float32; outputs rounded once.
+ *   Infinities and NaN among the valid tokens may also reach outputs of
+ *   earlier tokens of the same 128-token block.  The same call gives the same
+ *   bits.
+ */
+
+size_t vrwkv_decay_attn_workspace_bytes(int B, int T, int H, int D,
+                                        vrwkv_dtype dtype, int backward);
+
+/*
+ * vrwkv_decay_attn_fwd -- the form for whole sequences (prompts, training).
+ *   state      the states before the first token, or NULL for zeros.
+ *   out        (B, T, H*D).
+ *   state_out  the states after the last token, or NULL; may be `state`
+ *              itself (updated in place).
+ * Errors: INVALID_ARG for sizes <= 0, NULL or misaligned pointers, row strides
+ *   below H*D, a missing or small workspace, or an output (or the workspace)
+ *   that overlaps an input or another output; UNSUPPORTED beyond the limits
+ *   or for B*T or H*D >= 2^31.
+ */
+vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v,
+                                  long long ldq, long long ldk, long long ldv,
+                                  const float* w, const float* state,
+                                  const int* lengths, float scale, void* out,
+                                  float* state_out, int B, int T, int H, int D,
+                                  vrwkv_dtype dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * vrwkv_decay_attn_bwd -- the gradients of vrwkv_decay_attn_fwd for the
+ * upstream gradients gy = dL/dout and gstate = dL/dstate_out:
+ *   G_t  = e^{-w} G_{t+1} + scale q_t^T gy_t   (G_n: e^{-w} G_n = gstate)
+ *   gq_t = scale S_t gy_t,  gk_t = G_t v_t,  gv_t = G_t^T k_t,
+ *   gstate_in = e^{-w} G_0
+ * Nothing is kept from the forward call: its states are formed again.
+ *   state      as given to the forward call.
+ *   gstate     (B, H, D, D) or NULL for zeros.
+ *   gq, gk, gv (B, T, H*D) outputs, dtype `dtype`.
+ *   gstate_in  (B, H, D, D) gradient of `state`, or NULL.
+ * Errors: as vrwkv_decay_attn_fwd.
+ */
+vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v,
+                                  const void* gy, long long ldq, long long ldk,
+                                  long long ldv, long long ldg, const float* w,
+                                  const float* state, const float* gstate,
+                                  const int* lengths, float scale, void* gq,
+                                  void* gk, void* gv, float* gstate_in, int B,
+                                  int T, int H, int D, vrwkv_dtype dtype,
+                                  void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * vrwkv_decay_attn_step -- one token for each of B sequences (decoding), on a
+ * pool of N states that it updates in place.
+ *   q, k, v  (B, H*D), rows ldq, ldk, ldv elements apart.
+ *   state    (N, H, D, D) float32.
+ *   slots    int32[B] in device memory: sequence b's state is state[slots[b]];
+ *            NULL: state[b] (N >= B).  A negative slot marks an idle row: its
+ *            output is zeros and no state changes.  A slot >= N, or one that
+ *            an earlier row names too, is handled as an idle row and sets flag
+ *            16 of the device error word (vrwkv_device_status).
+ *   out      (B, H*D) dense.
+ * Errors: as vrwkv_decay_attn_fwd, plus INVALID_ARG for N <= 0, or N < B
+ *   without slots.
+ */
+vrwkv_status vrwkv_decay_attn_step(const void* q, const void* k, const void* v,
+                                   long long ldq, long long ldk, long long ldv,
+                                   const float* w, float* state,
+                                   const int* slots, float scale, void* out,
+                                   int B, int N, int H, int D,
+                                   vrwkv_dtype dtype, void* stream);
+
+/*
+ * vrwkv_layer_norm_fwd -- the LayerNorm of vrwkv_spatial_mix_block as an
+ * operation of its own, over the C channels of each row:
+ *   y = gamma * (x - mean) * rstd + beta,  rstd = 1 / sqrt(var + eps)
+ * with the biased variance.
+ *   x, y        (rows, C) dense, dtype `dtype`.
+ *   gamma, beta float32[C]; eps >= 0.
+ *   mean, rstd  float32[rows] outputs for the backward pass, or both NULL.
+ * Errors: INVALID_ARG for sizes <= 0, NULL or misaligned pointers, a negative
+ *   eps, mean without rstd, or an output that overlaps an input or another
+ *   output; UNSUPPORTED for rows >= 2^31.
+ */
+vrwkv_status vrwkv_layer_norm_fwd(const void* x, const float* gamma,
+                                  const float* beta, float eps, void* y,
+                                  float* mean, float* rstd, long long rows,
+                                  int C, vrwkv_dtype dtype, void* stream);
+
+/*
+ * vrwkv_layer_norm_bwd -- gradients of vrwkv_layer_norm_fwd.  With xh =
+ * (x - mean) rstd, d = gamma gy and means over the channels of a row:
+ *   gx = rstd (d - mean(d) - xh mean(d xh))
+ *   ggamma = sum_rows gy xh,  gbeta = sum_rows gy
+ *   x, gy, gx      (rows, C) dense, dtype `dtype`.
+ *   mean, rstd     float32[rows] from the forward call.
+ *   ggamma, gbeta  float32[C] outputs, or both NULL; the rows are summed in a
+ *                  fixed order (the same call gives the same bits).
+ *   workspace      device memory of at least
+ *                  vrwkv_layer_norm_bwd_workspace_bytes(rows, C, dtype) bytes,
+ *                  256-byte aligned (NULL without ggamma and gbeta); no
+ *                  preparation; separate ones for calls that may run at the
+ *                  same time.
+ * Limits: C <= 8192 (UNSUPPORTED above).
+ * Errors: as vrwkv_layer_norm_fwd, plus INVALID_ARG for a missing or small
+ *   workspace.
+ */
+size_t vrwkv_layer_norm_bwd_workspace_bytes(long long rows, int C,
+                                            vrwkv_dtype dtype);
+
+vrwkv_status vrwkv_layer_norm_bwd(const void* x, const float* gamma,
+                                  const float* mean, const float* rstd,
+                                  const void* gy, void* gx, float* ggamma,
+                                  float* gbeta, long long rows, int C,
+                                  vrwkv_dtype dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
  * vrwkv_device_status -- report and clear kernel-side failures on the
  * current device.  Kernels that wait for their asynchronous (TMA) tile
  * copies (bit 0) or, in the workspace variants, for the records of the other
@@ -441,10 +595,11 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  * variant that finds its workspace in an invalid state (not zero-filled
  * before first use; bit 2) stops at once.  Each records the failure in a
  * device error word and finishes (its outputs are then undefined) instead
- * of hanging.  This call synchronises with the current device, reads that
+ * of hanging.  vrwkv_decay_attn_step records a slot it could not use (bit 4).
+ * This call synchronises with the current device, reads that
  * word, clears it and returns VRWKV_ERR_TIMEOUT if it was set, VRWKV_OK
- * otherwise (VRWKV_ERR_CUDA if the device cannot be read); the bits are in
- * vrwkv_last_error().
+ * otherwise (VRWKV_ERR_INVALID_ARG if bit 4 alone was set, VRWKV_ERR_CUDA if
+ * the device cannot be read); the bits are in vrwkv_last_error().
  */
 vrwkv_status vrwkv_device_status(void);
 

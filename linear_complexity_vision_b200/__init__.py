@@ -14,6 +14,11 @@ There is no fallback: if the library is missing, the calls raise.
     channel_mix(x, qs=None)
     biwkv_bwd(k, v, w, u, gy)  # -> gk, gv, gw (B, C), gu (B, C), gw_total, gu_total
     spatial_mix_block(x, weights, w, u, ln_gamma, ln_beta, qs, workspace=None)
+    decay_attn_fwd(q, k, v, w, heads, scale=1.0, state=None, lengths=None)  # -> out, final state
+    decay_attn_bwd(q, k, v, w, heads, gy, scale=1.0, state=None, gstate=None, lengths=None)
+    decay_attn_step(q, k, v, w, heads, state, slots=None, scale=1.0)  # one token, states in place
+    layer_norm_fwd(x, gamma, beta, eps=1e-5)  # -> y, mean, rstd
+    layer_norm_bwd(x, gamma, mean, rstd, gy)  # -> gx, ggamma, gbeta
     device_status()     # synchronise; raise if a kernel's bounded wait ran out
 
 Token tensors are contiguous (B, T, C) CUDA tensors of dtype float32 or
@@ -98,6 +103,21 @@ def load_library():
         lib.vrwkv_biwkv_bwd.restype = ci
         lib.vrwkv_channel_mix.argtypes = [vp, vp, ci, ci, ci, ci, ctypes.POINTER(_QsParams), vp]
         lib.vrwkv_channel_mix.restype = ci
+        ll, cs, cf = ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float
+        lib.vrwkv_decay_attn_workspace_bytes.argtypes = [ci] * 6
+        lib.vrwkv_decay_attn_workspace_bytes.restype = cs
+        lib.vrwkv_decay_attn_fwd.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 3 + [cf] + [vp] * 2 + [ci] * 5 + [vp, cs, vp]
+        lib.vrwkv_decay_attn_fwd.restype = ci
+        lib.vrwkv_decay_attn_bwd.argtypes = [vp] * 4 + [ll] * 4 + [vp] * 4 + [cf] + [vp] * 4 + [ci] * 5 + [vp, cs, vp]
+        lib.vrwkv_decay_attn_bwd.restype = ci
+        lib.vrwkv_decay_attn_step.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 3 + [cf, vp] + [ci] * 5 + [vp]
+        lib.vrwkv_decay_attn_step.restype = ci
+        lib.vrwkv_layer_norm_fwd.argtypes = [vp] * 3 + [cf] + [vp] * 3 + [ll, ci, ci, vp]
+        lib.vrwkv_layer_norm_fwd.restype = ci
+        lib.vrwkv_layer_norm_bwd_workspace_bytes.argtypes = [ll, ci, ci]
+        lib.vrwkv_layer_norm_bwd_workspace_bytes.restype = cs
+        lib.vrwkv_layer_norm_bwd.argtypes = [vp] * 8 + [ll, ci, ci, vp, cs, vp]
+        lib.vrwkv_layer_norm_bwd.restype = ci
         lib.vrwkv_device_status.argtypes = []
         lib.vrwkv_device_status.restype = ci
         lib.vrwkv_set_wait_limit.argtypes = [ctypes.c_double]
@@ -450,6 +470,297 @@ def biwkv_bwd(k, v, w, u, gy, totals: bool = True, out=None):
         gv.data_ptr(), gw.data_ptr(), gu.data_ptr(), None if gwt is None else gwt.data_ptr(),
         None if gut is None else gut.data_ptr(), B, T, C, _dtype_code(k), _stream_ptr(k)))
     return gk, gv, gw, gu, gwt, gut
+
+
+def _require_rows(name, t, shape, dtype, device) -> int:
+    """Row stride in elements of a token tensor whose rows of C channels are
+    evenly spaced: contiguous, or a column slice of a wider tensor."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {tuple(shape)} tensor of {dtype}")
+    C = shape[-1]
+    if t.is_contiguous():
+        return C
+    stride = t.stride()
+    if C > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: the channels of a row must be adjacent")
+    # the rows' spacing, from the innermost dimension that has more than one
+    ld, rows = None, 1
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n > 1:
+            if ld is None:
+                ld = s // rows if s % rows == 0 else -1
+            if s != ld * rows:
+                raise ValueError(f"{name}: the rows must be evenly spaced")
+        rows *= n
+    if ld is None:
+        return C
+    if ld < C:
+        raise ValueError(f"{name}: rows must not overlap")
+    return ld
+
+
+def _require_f32(name, t, shape, device) -> None:
+    import torch
+    _require(t, name)
+    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must be a float32 tensor of shape {tuple(shape)} on {device}")
+
+
+def _require_ints(name, t, n, device) -> None:
+    import torch
+    _require(t, name)
+    if t.dtype != torch.int32 or tuple(t.shape) != (n,) or t.device != device:
+        raise ValueError(f"{name} must be an int32 tensor of {n} elements on {device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _on:
+    """Make a tensor's device the current one for a call."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        import torch
+        now = torch.cuda.current_device()
+        self.back = now if self.device.index is not None and self.device.index != now else None
+        if self.back is not None:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        import torch
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _heads(shape, heads: int, what: str) -> int:
+    heads = int(heads)
+    if heads <= 0 or shape[-1] % heads != 0:
+        raise ValueError(f"{what} must have a whole number of channels for each of {heads} heads")
+    return shape[-1] // heads
+
+
+def _workspace(need: int, workspace, device):
+    """The caller's workspace, or a new one of `need` bytes (None for 0)."""
+    import torch
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _require(workspace, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return workspace
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def decay_attn_workspace(B: int, T: int, heads: int, head_size: int, dtype, backward: bool = False, device="cuda"):
+    """A uint8 CUDA tensor usable as the workspace of decay_attn_fwd (or, with
+    backward, decay_attn_bwd) on problems of these sizes, one call at a time."""
+    import torch
+    device = torch.empty(0, device=device).device
+    code = VRWKV_F32 if dtype == torch.float32 else VRWKV_BF16
+    with _on(device):
+        n = int(load_library().vrwkv_decay_attn_workspace_bytes(B, T, int(heads), int(head_size), code, int(backward)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def decay_attn_fwd(q, k, v, w, heads: int, scale: float = 1.0, state=None, lengths=None, want_state: bool = True,
+                   out=None, state_out=None, workspace=None):
+    """Multi-head decay attention of whole sequences: per head, S_t = e^{-w}
+    S_{t-1} + k_t^T v_t and out_t = scale q_t S_t (vrwkv_decay_attn_fwd).
+
+    q, k, v: (B, T, C), C = heads * D, D <= 128, rows evenly spaced (contiguous
+    or column slices of one projection); w: float32 (heads,).  state: float32
+    (B, heads, D, D) before the first token, default zeros.  lengths: int32
+    (B,), sequence b's valid tokens; rows past them are not used and give zeros.
+    Returns out (B, T, C) and the state after the last token (state_out if
+    given; it may be state itself; None if not wanted)."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be a (B, T, C) tensor")
+    B, T, C = q.shape
+    D = _heads(q.shape, heads, "q")
+    dev, code = q.device, _dtype_code(q)
+    ld = [_require_rows(n, t, q.shape, q.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
+    _require_vec(w, heads, dev, "w")
+    shape = (B, heads, D, D)
+    for n, t in (("state", state), ("state_out", state_out)):
+        if t is not None:
+            _require_f32(n, t, shape, dev)
+    if lengths is not None:
+        _require_ints("lengths", lengths, B, dev)
+    if out is None:
+        out = torch.empty((B, T, C), dtype=q.dtype, device=dev)
+    else:
+        _require(out, "out")
+        if out.shape != q.shape or out.dtype != q.dtype or out.device != dev:
+            raise ValueError("out must match q in shape, dtype and device")
+    if state_out is None and want_state:
+        state_out = torch.empty(shape, dtype=torch.float32, device=dev)
+    lib = load_library()
+    with _on(dev):
+        need = 0 if workspace is not None else int(lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 0))
+        ws = _workspace(need, workspace, dev)
+        _check(lib.vrwkv_decay_attn_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), *ld, w.data_ptr(), _ptr(state), _ptr(lengths), float(scale),
+            out.data_ptr(), _ptr(state_out), B, T, heads, D, code, *_ws_args(ws), _stream_ptr(q)))
+    return out, state_out
+
+
+def decay_attn_bwd(q, k, v, w, heads: int, gy, scale: float = 1.0, state=None, gstate=None, lengths=None, out=None,
+                   workspace=None):
+    """Gradients of decay_attn_fwd for gy = dL/dout and, optionally, gstate =
+    dL/d(final state) (vrwkv_decay_attn_bwd): gq, gk, gv (B, T, C) and, if state
+    is given, its gradient (else None).  w is a constant: no gradient.
+    out: optional (gq, gk, gv, gstate_in or None) to write instead of
+    allocating them."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be a (B, T, C) tensor")
+    B, T, C = q.shape
+    D = _heads(q.shape, heads, "q")
+    dev, code = q.device, _dtype_code(q)
+    ld = [_require_rows(n, t, q.shape, q.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v), ("gy", gy))]
+    _require_vec(w, heads, dev, "w")
+    shape = (B, heads, D, D)
+    if out is None:
+        gq, gk, gv = (torch.empty((B, T, C), dtype=q.dtype, device=dev) for _ in range(3))
+        gs = None if state is None else torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        gq, gk, gv, gs = out
+        for n, t in (("gq", gq), ("gk", gk), ("gv", gv)):
+            _require(t, n)
+            if t.shape != q.shape or t.dtype != q.dtype or t.device != dev:
+                raise ValueError(f"{n} must match q in shape, dtype and device")
+    for n, t in (("state", state), ("gstate", gstate), ("gstate_in", gs)):
+        if t is not None:
+            _require_f32(n, t, shape, dev)
+    if lengths is not None:
+        _require_ints("lengths", lengths, B, dev)
+    lib = load_library()
+    with _on(dev):
+        need = 0 if workspace is not None else int(lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 1))
+        ws = _workspace(need, workspace, dev)
+        _check(lib.vrwkv_decay_attn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), gy.data_ptr(), *ld, w.data_ptr(), _ptr(state), _ptr(gstate),
+            _ptr(lengths), float(scale), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gs), B, T, heads, D, code,
+            *_ws_args(ws), _stream_ptr(q)))
+    return gq, gk, gv, gs
+
+
+def decay_attn_step(q, k, v, w, heads: int, state, slots=None, scale: float = 1.0, out=None):
+    """One token of each of B sequences (vrwkv_decay_attn_step): q, k, v (B, C);
+    state: a pool (N, heads, D, D) of float32 states, updated in place; slots:
+    int32 (B,), sequence b's place in it (default b).  A negative slot marks an
+    idle row, whose output is zeros; a slot >= N or named by an earlier row too
+    is treated so and reported by device_status().  Returns out (B, C)."""
+    import torch
+    if q.dim() != 2:
+        raise ValueError("q must be a (B, C) tensor")
+    B, C = q.shape
+    D = _heads(q.shape, heads, "q")
+    dev, code = q.device, _dtype_code(q)
+    ld = [_require_rows(n, t, q.shape, q.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
+    _require_vec(w, heads, dev, "w")
+    if state.dim() != 4:
+        raise ValueError("state must be a (N, heads, D, D) tensor")
+    N = state.shape[0]
+    _require_f32("state", state, (N, heads, D, D), dev)
+    if slots is not None:
+        _require_ints("slots", slots, B, dev)
+    if out is None:
+        out = torch.empty((B, C), dtype=q.dtype, device=dev)
+    else:
+        _require(out, "out")
+        if out.shape != q.shape or out.dtype != q.dtype or out.device != dev:
+            raise ValueError("out must match q in shape, dtype and device")
+    with _on(dev):
+        _check(load_library().vrwkv_decay_attn_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), *ld, w.data_ptr(), state.data_ptr(), _ptr(slots), float(scale),
+            out.data_ptr(), B, N, heads, D, code, _stream_ptr(q)))
+    return out
+
+
+def _norm_rows(x):
+    _require(x, "x")
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError("x must be a (..., C) tensor with rows")
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def layer_norm_fwd(x, gamma, beta, eps: float = 1e-5, stats: bool = True, out=None):
+    """LayerNorm over the last dimension of a contiguous (..., C) tensor
+    (vrwkv_layer_norm_fwd), gamma and beta float32 (C,).  Returns y and the rows'
+    mean and rstd (float32, x's shape without C; None without stats)."""
+    import torch
+    rows, C = _norm_rows(x)
+    dev = x.device
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        _require_vec(t, C, dev, name)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _require(out, "out")
+        if out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
+            raise ValueError("out must match x in shape, dtype and device")
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
+    with _on(dev):
+        _check(load_library().vrwkv_layer_norm_fwd(
+            x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), float(eps), out.data_ptr(), _ptr(mean), _ptr(rstd), rows,
+            C, _dtype_code(x), _stream_ptr(x)))
+    return out, mean, rstd
+
+
+def layer_norm_bwd_workspace(rows: int, C: int, dtype, device="cuda"):
+    """A uint8 CUDA tensor usable as layer_norm_bwd's workspace, one call at a
+    time."""
+    import torch
+    device = torch.empty(0, device=device).device
+    code = VRWKV_F32 if dtype == torch.float32 else VRWKV_BF16
+    with _on(device):
+        n = int(load_library().vrwkv_layer_norm_bwd_workspace_bytes(rows, C, code))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def layer_norm_bwd(x, gamma, mean, rstd, gy, weight_grads: bool = True, out=None, workspace=None):
+    """Gradients of layer_norm_fwd (vrwkv_layer_norm_bwd) from the mean and rstd
+    it returned: gx like x, ggamma and gbeta float32 (C,) (None without
+    weight_grads).  out: optional gx to write instead of allocating it."""
+    import torch
+    rows, C = _norm_rows(x)
+    dev = x.device
+    _require_vec(gamma, C, dev, "gamma")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _require_vec(t, rows, dev, name)
+    _require(gy, "gy")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _require(out, "out")
+    for t, name in ((gy, "gy"), (out, "out")):
+        if t.shape != x.shape or t.dtype != x.dtype or t.device != dev:
+            raise ValueError(f"{name} must match x in shape, dtype and device")
+    code = _dtype_code(x)
+    ggamma = torch.empty(C, dtype=torch.float32, device=dev) if weight_grads else None
+    gbeta = torch.empty(C, dtype=torch.float32, device=dev) if weight_grads else None
+    lib = load_library()
+    with _on(dev):
+        need = 0
+        if weight_grads and workspace is None:
+            need = int(lib.vrwkv_layer_norm_bwd_workspace_bytes(rows, C, code))
+        ws = _workspace(need, workspace, dev)
+        _check(lib.vrwkv_layer_norm_bwd(
+            x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), gy.data_ptr(), out.data_ptr(),
+            _ptr(ggamma), _ptr(gbeta), rows, C, code, *_ws_args(ws), _stream_ptr(x)))
+    return out, ggamma, gbeta
 
 
 def set_wait_limit(seconds: float) -> None:

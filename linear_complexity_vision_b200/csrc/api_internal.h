@@ -1,0 +1,60 @@
+// Host-side helpers of the C ABI shared by its translation units: the
+// thread's last error and kernel, argument checks, and per-device lookups.
+// Defined in vrwkv_api.cu unless noted.
+#pragma once
+
+#include <atomic>
+#include <cstddef>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "vrwkv.h"
+
+namespace vrwkv {
+namespace api {
+
+// Record the reason of a non-OK status (printf-style) and return it.
+vrwkv_status fail(vrwkv_status s, const char* fmt, ...);
+vrwkv_status ok();
+vrwkv_status cuda_status(cudaError_t e, const char* what);
+void set_last_kernel(const char* name);
+
+bool aligned(const void* p, size_t a);
+bool overlaps(const void* a, size_t na, const void* b, size_t nb);
+int elem_bytes(vrwkv_dtype dt);
+
+// Current device: its SM count, its error word (nullptr if unknown) and the
+// limit of bounded waits in nanoseconds.
+int sm_count();
+unsigned int* device_error_word();
+constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
+unsigned long long wait_limit_ns();
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();  // nullptr if the driver does not offer it
+
+// Raise the dynamic shared-memory limit of a kernel once per size needed.
+template <typename K>
+cudaError_t ensure_smem(K kernel, std::atomic<int>& granted, int bytes) {
+    if (bytes <= 48 * 1024 || bytes <= granted.load(std::memory_order_relaxed)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) {
+        int cur = granted.load();
+        while (bytes > cur && !granted.compare_exchange_weak(cur, bytes)) {
+        }
+    }
+    return e;
+}
+
+}  // namespace api
+
+// The LayerNorm forward launch (layer_norm_api.cu); its arguments are checked.
+struct LayerNormParams;
+namespace api {
+vrwkv_status launch_layer_norm(const LayerNormParams& p, vrwkv_dtype dtype, cudaStream_t s);
+}  // namespace api
+}  // namespace vrwkv

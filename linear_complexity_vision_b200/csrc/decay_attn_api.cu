@@ -1,0 +1,359 @@
+// C ABI of the multi-head decay attention (declared in include/vrwkv.h):
+// host-side argument validation, the cut into segments and kernel launches.
+// Validation happens before any CUDA call.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "api_internal.h"
+#include "decay_attn.cuh"
+
+namespace {
+
+using namespace vrwkv;
+using namespace vrwkv::api;
+
+constexpr int kMaxD = 128;
+constexpr int kSegUnit = 128;  // segments are multiples of this many tokens
+
+struct Span {
+    const void* p;
+    size_t n;
+};
+
+// Bytes a (B, T, C) tensor spans whose rows lie ld elements apart.
+size_t span_bytes(int B, int T, int C, long long ld, int es) {
+    return (((size_t)B * T - 1) * (size_t)ld + C) * es;
+}
+
+vrwkv_status check_sizes(int B, int T, int H, int D, vrwkv_dtype dtype) {
+    if (dtype != VRWKV_F32 && dtype != VRWKV_BF16)
+        return fail(VRWKV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (B <= 0 || T <= 0 || H <= 0 || D <= 0)
+        return fail(VRWKV_ERR_INVALID_ARG, "B, T, H and D must be positive (got %d, %d, %d, %d)", B, T, H, D);
+    if (D > kMaxD) return fail(VRWKV_ERR_UNSUPPORTED, "head size D = %d exceeds %d", D, kMaxD);
+    if ((long long)B * T > INT_MAX || (long long)H * D > INT_MAX)
+        return fail(VRWKV_ERR_UNSUPPORTED, "B*T and H*D must be below 2^31");
+    return ok();
+}
+
+// Every output against every input and every other output.
+vrwkv_status check_overlaps(const Span* outs, int no, const Span* ins, int ni) {
+    for (int i = 0; i < no; ++i) {
+        for (int j = 0; j < ni; ++j)
+            if (overlaps(outs[i].p, outs[i].n, ins[j].p, ins[j].n))
+                return fail(VRWKV_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+        for (int j = i + 1; j < no; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+                return fail(VRWKV_ERR_INVALID_ARG, "outputs or the workspace overlap");
+    }
+    return ok();
+}
+
+vrwkv_status check_workspace(const void* ws, size_t have, size_t need) {
+    if (!need) return ok();
+    if (!ws) return fail(VRWKV_ERR_INVALID_ARG, "required pointer is NULL (workspace)");
+    if (!aligned(ws, 256)) return fail(VRWKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (have < need)
+        return fail(VRWKV_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", have, need);
+    return ok();
+}
+
+// ---- the cut into segments ----
+int padded_d(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
+
+struct Cut {
+    int seg_tokens, nseg;
+};
+Cut cut_into(int T, int want) {
+    const int units = (T + kSegUnit - 1) / kSegUnit;
+    const int per = (units + std::max(1, std::min(want, units)) - 1) / std::max(1, std::min(want, units));
+    return Cut{per * kSegUnit, (units + per - 1) / per};
+}
+
+// One head's chunks run one after the other; segments let more CTAs than
+// heads work.  As many as fill the SMs once with resident CTAs.
+Cut plan_f32(int B, int T, int H, int D, int nprob) {
+    const int resident = padded_d(D) == 128 ? 1 : 4;
+    const long long heads = (long long)B * H * nprob;
+    const long long slots = (long long)sm_count() * resident;
+    return cut_into(T, (int)std::max<long long>(1, slots / heads));
+}
+
+size_t state_floats(int B, int H, int D, int nseg) { return (size_t)B * H * nseg * D * D; }
+
+size_t ws_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
+    const Cut c = plan_f32(B, T, H, D, backward ? 3 : 1);
+    if (c.nseg == 1) return 0;
+    return ((backward ? 2 : 1) * state_floats(B, H, D, c.nseg) * 4 + 255) / 256 * 256;
+}
+
+// ---- launches ----
+template <typename IO, int DP>
+vrwkv_status launch_dp(const decay::Params& p, long long ctas, cudaStream_t s) {
+    static std::atomic<int> granted{0};
+    constexpr int smem = decay::Cfg<DP>::kSmemFloats * 4;
+    const cudaError_t e = ensure_smem(decay::decay_attn_kernel<IO, DP>, granted, smem);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    decay::decay_attn_kernel<IO, DP><<<(unsigned)ctas, decay::Cfg<DP>::kThreads, smem, s>>>(p);
+    return cuda_status(cudaGetLastError(), "decay_attn_kernel launch");
+}
+
+template <typename IO>
+vrwkv_status launch_io(const decay::Params& p, cudaStream_t s) {
+    const long long ctas = (long long)p.B * p.H * p.nseg * p.nprob;
+    if (ctas > INT_MAX) return fail(VRWKV_ERR_UNSUPPORTED, "too many heads (B*H = %lld)", (long long)p.B * p.H);
+    switch (padded_d(p.D)) {
+    case 32: return launch_dp<IO, 32>(p, ctas, s);
+    case 64: return launch_dp<IO, 64>(p, ctas, s);
+    default: return launch_dp<IO, 128>(p, ctas, s);
+    }
+}
+
+vrwkv_status launch_attn(const decay::Params& p, vrwkv_dtype dtype, cudaStream_t s) {
+    return dtype == VRWKV_F32 ? launch_io<float>(p, s) : launch_io<__nv_bfloat16>(p, s);
+}
+
+vrwkv_status launch_chain(const decay::ChainParams& p, int bh, int nprob, cudaStream_t s) {
+    decay::decay_chain_kernel<<<dim3((unsigned)bh, (unsigned)((p.dd + 255) / 256), (unsigned)nprob), 256, 0, s>>>(p);
+    return cuda_status(cudaGetLastError(), "decay_chain_kernel launch");
+}
+
+bool vec_ok(const void* p, long long ld, int es) { return aligned(p, 4 * es) && ld % 4 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t vrwkv_decay_attn_workspace_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, int backward) {
+    if (B <= 0 || T <= 0 || H <= 0 || D <= 0 || D > kMaxD || (dtype != VRWKV_F32 && dtype != VRWKV_BF16)) return 0;
+    return ws_bytes(B, T, H, D, dtype, backward != 0);
+}
+
+vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, long long ldq, long long ldk,
+                                  long long ldv, const float* w, const float* state, const int* lengths, float scale,
+                                  void* out, float* state_out, int B, int T, int H, int D, vrwkv_dtype dtype,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    vrwkv_status st = check_sizes(B, T, H, D, dtype);
+    if (st != VRWKV_OK) return st;
+    if (!q || !k || !v || !w || !out) return fail(VRWKV_ERR_INVALID_ARG, "required pointer is NULL");
+    const int es = elem_bytes(dtype), C = H * D;
+    if (ldq < C || ldk < C || ldv < C) return fail(VRWKV_ERR_INVALID_ARG, "a row stride is below H*D = %d", C);
+    const void* toks[4] = {q, k, v, out};
+    for (const void* t : toks)
+        if (!aligned(t, es)) return fail(VRWKV_ERR_INVALID_ARG, "token tensor misaligned");
+    const void* words[4] = {w, state, lengths, state_out};
+    for (const void* f : words)
+        if (f && !aligned(f, 4)) return fail(VRWKV_ERR_INVALID_ARG, "float32 or int32 array misaligned");
+    const size_t need = ws_bytes(B, T, H, D, dtype, false);
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != VRWKV_OK) return st;
+    const size_t nb = span_bytes(B, T, C, C, es), ns = state_floats(B, H, D, 1) * 4;
+    const bool in_place = state_out && state_out == state;
+    const Span ins[6] = {{q, span_bytes(B, T, C, ldq, es)}, {k, span_bytes(B, T, C, ldk, es)},
+                         {v, span_bytes(B, T, C, ldv, es)}, {w, (size_t)H * 4},
+                         {lengths, (size_t)B * 4},          {in_place ? nullptr : state, ns}};
+    const Span outs[3] = {{out, nb}, {state_out, ns}, {workspace, need}};
+    st = check_overlaps(outs, 3, ins, 6);
+    if (st != VRWKV_OK) return st;
+
+    const Cut cut = plan_f32(B, T, H, D, 1);
+    decay::Params p = {};
+    p.w = w;
+    p.lengths = lengths;
+    p.B = B;
+    p.T = T;
+    p.H = H;
+    p.D = D;
+    p.seg_tokens = cut.seg_tokens;
+    p.nseg = cut.nseg;
+    p.nprob = 1;
+    p.vec = D % 4 == 0 && vec_ok(q, ldq, es) && vec_ok(k, ldk, es) && vec_ok(v, ldv, es) && vec_ok(out, C, es);
+    decay::Problem& pr = p.pr[0];
+    pr.q = static_cast<const char*>(q);
+    pr.k = static_cast<const char*>(k);
+    pr.v = static_cast<const char*>(v);
+    pr.ldq = ldq;
+    pr.ldk = ldk;
+    pr.ldv = ldv;
+    pr.scale_intra = pr.scale_inter = scale;
+    pr.scale_upd = 1.0f;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* ws = static_cast<float*>(workspace);
+    if (cut.nseg > 1) {
+        pr.x_out = ws;
+        st = launch_attn(p, dtype, s);
+        if (st != VRWKV_OK) return st;
+        decay::ChainParams c = {};
+        c.pr[0] = {ws, state, state_out, 0};
+        c.w = w;
+        c.lengths = lengths;
+        c.T = T;
+        c.H = H;
+        c.dd = D * D;
+        c.seg_tokens = cut.seg_tokens;
+        c.nseg = cut.nseg;
+        st = launch_chain(c, B * H, 1, s);
+        if (st != VRWKV_OK) return st;
+        pr.x_in = ws;
+        pr.x_out = nullptr;
+    } else {
+        pr.x_in = state;
+        pr.x_out = state_out;
+    }
+    pr.out = static_cast<char*>(out);
+    st = launch_attn(p, dtype, s);
+    if (st == VRWKV_OK) set_last_kernel("decay_attn_kernel");
+    return st;
+}
+
+vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, const void* gy, long long ldq,
+                                  long long ldk, long long ldv, long long ldg, const float* w, const float* state,
+                                  const float* gstate, const int* lengths, float scale, void* gq, void* gk, void* gv,
+                                  float* gstate_in, int B, int T, int H, int D, vrwkv_dtype dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    vrwkv_status st = check_sizes(B, T, H, D, dtype);
+    if (st != VRWKV_OK) return st;
+    if (!q || !k || !v || !gy || !w || !gq || !gk || !gv)
+        return fail(VRWKV_ERR_INVALID_ARG, "required pointer is NULL");
+    const int es = elem_bytes(dtype), C = H * D;
+    if (ldq < C || ldk < C || ldv < C || ldg < C)
+        return fail(VRWKV_ERR_INVALID_ARG, "a row stride is below H*D = %d", C);
+    const void* toks[7] = {q, k, v, gy, gq, gk, gv};
+    for (const void* t : toks)
+        if (!aligned(t, es)) return fail(VRWKV_ERR_INVALID_ARG, "token tensor misaligned");
+    const void* words[5] = {w, state, gstate, lengths, gstate_in};
+    for (const void* f : words)
+        if (f && !aligned(f, 4)) return fail(VRWKV_ERR_INVALID_ARG, "float32 or int32 array misaligned");
+    const size_t need = ws_bytes(B, T, H, D, dtype, true);
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != VRWKV_OK) return st;
+    const size_t nb = span_bytes(B, T, C, C, es), ns = state_floats(B, H, D, 1) * 4;
+    const Span ins[8] = {{q, span_bytes(B, T, C, ldq, es)}, {k, span_bytes(B, T, C, ldk, es)},
+                         {v, span_bytes(B, T, C, ldv, es)}, {gy, span_bytes(B, T, C, ldg, es)},
+                         {w, (size_t)H * 4},                {lengths, (size_t)B * 4},
+                         {state, ns},                       {gstate, ns}};
+    const Span outs[5] = {{gq, nb}, {gk, nb}, {gv, nb}, {gstate_in, ns}, {workspace, need}};
+    st = check_overlaps(outs, 5, ins, 8);
+    if (st != VRWKV_OK) return st;
+
+    const Cut cut = plan_f32(B, T, H, D, 3);
+    decay::Params p = {};
+    p.w = w;
+    p.lengths = lengths;
+    p.B = B;
+    p.T = T;
+    p.H = H;
+    p.D = D;
+    p.seg_tokens = cut.seg_tokens;
+    p.nseg = cut.nseg;
+    p.vec = D % 4 == 0 && vec_ok(q, ldq, es) && vec_ok(k, ldk, es) && vec_ok(v, ldv, es) && vec_ok(gy, ldg, es) &&
+            vec_ok(gq, C, es) && vec_ok(gk, C, es) && vec_ok(gv, C, es);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const char* Q = static_cast<const char*>(q);
+    const char* K = static_cast<const char*>(k);
+    const char* V = static_cast<const char*>(v);
+    const char* G = static_cast<const char*>(gy);
+    const float* s_in = state;   // X_in of the segments: S of the forward pass
+    const float* g_in = gstate;  // and dL/dS of the reversed one
+    float* g_out = gstate_in;
+    if (cut.nseg > 1) {
+        float* ws = static_cast<float*>(workspace);
+        float* wg = ws + state_floats(B, H, D, cut.nseg);
+        decay::Problem& a = p.pr[0];
+        a.k = K;
+        a.ldk = ldk;
+        a.v = V;
+        a.ldv = ldv;
+        a.x_out = ws;
+        a.scale_upd = 1.0f;
+        decay::Problem& c = p.pr[1];
+        c.k = Q;
+        c.ldk = ldq;
+        c.v = G;
+        c.ldv = ldg;
+        c.x_out = wg;
+        c.scale_upd = scale;
+        c.reverse = 1;
+        p.nprob = 2;
+        st = launch_attn(p, dtype, s);
+        if (st != VRWKV_OK) return st;
+        decay::ChainParams cp = {};
+        cp.pr[0] = {ws, state, nullptr, 0};
+        cp.pr[1] = {wg, gstate, gstate_in, 1};
+        cp.w = w;
+        cp.lengths = lengths;
+        cp.T = T;
+        cp.H = H;
+        cp.dd = D * D;
+        cp.seg_tokens = cut.seg_tokens;
+        cp.nseg = cut.nseg;
+        st = launch_chain(cp, B * H, 2, s);
+        if (st != VRWKV_OK) return st;
+        s_in = ws;
+        g_in = wg;
+        g_out = nullptr;
+    }
+    p.nprob = 3;
+    // gq: (g, v, k) forward in time on S^T
+    p.pr[0] = {G, V, K, static_cast<char*>(gq), ldg, ldv, ldk, s_in, nullptr, 1, 1, 0, scale, scale, 1.0f};
+    // gk: (v, g, q) in reversed time on (dL/dS)^T; gv: (k, q, g) on dL/dS
+    p.pr[1] = {V, G, Q, static_cast<char*>(gk), ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale};
+    p.pr[2] = {K, Q, G, static_cast<char*>(gv), ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale};
+    st = launch_attn(p, dtype, s);
+    if (st == VRWKV_OK) set_last_kernel("decay_attn_kernel");
+    return st;
+}
+
+vrwkv_status vrwkv_decay_attn_step(const void* q, const void* k, const void* v, long long ldq, long long ldk,
+                                   long long ldv, const float* w, float* state, const int* slots, float scale,
+                                   void* out, int B, int N, int H, int D, vrwkv_dtype dtype, void* stream) {
+    vrwkv_status st = check_sizes(B, 1, H, D, dtype);
+    if (st != VRWKV_OK) return st;
+    if (N <= 0) return fail(VRWKV_ERR_INVALID_ARG, "the pool must hold at least one state (got %d)", N);
+    if (!slots && N < B)
+        return fail(VRWKV_ERR_INVALID_ARG, "without slots the pool must hold B = %d states (got %d)", B, N);
+    if (!q || !k || !v || !w || !state || !out) return fail(VRWKV_ERR_INVALID_ARG, "required pointer is NULL");
+    if (H > 65535) return fail(VRWKV_ERR_UNSUPPORTED, "H = %d exceeds 65535", H);
+    const int es = elem_bytes(dtype), C = H * D;
+    if (ldq < C || ldk < C || ldv < C) return fail(VRWKV_ERR_INVALID_ARG, "a row stride is below H*D = %d", C);
+    const void* toks[4] = {q, k, v, out};
+    for (const void* t : toks)
+        if (!aligned(t, es)) return fail(VRWKV_ERR_INVALID_ARG, "token tensor misaligned");
+    const void* words[3] = {w, state, slots};
+    for (const void* f : words)
+        if (f && !aligned(f, 4)) return fail(VRWKV_ERR_INVALID_ARG, "float32 or int32 array misaligned");
+    const Span ins[5] = {{q, span_bytes(B, 1, C, ldq, es)}, {k, span_bytes(B, 1, C, ldk, es)},
+                         {v, span_bytes(B, 1, C, ldv, es)}, {w, (size_t)H * 4}, {slots, (size_t)B * 4}};
+    const Span outs[2] = {{out, (size_t)B * C * es}, {state, state_floats(N, H, D, 1) * 4}};
+    st = check_overlaps(outs, 2, ins, 5);
+    if (st != VRWKV_OK) return st;
+    decay::StepParams p;
+    p.q = static_cast<const char*>(q);
+    p.k = static_cast<const char*>(k);
+    p.v = static_cast<const char*>(v);
+    p.out = static_cast<char*>(out);
+    p.ldq = ldq;
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.w = w;
+    p.state = state;
+    p.slots = slots;
+    p.B = B;
+    p.N = N;
+    p.H = H;
+    p.D = D;
+    p.scale = scale;
+    p.vec = D % 4 == 0 && aligned(state, 16);
+    p.err = device_error_word();
+    if (!p.err) return fail(VRWKV_ERR_CUDA, "cannot locate the device error word");
+    const dim3 grid((unsigned)B, (unsigned)H, (unsigned)((D + decay::kStepCols - 1) / decay::kStepCols));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == VRWKV_F32) decay::decay_step_kernel<float><<<grid, decay::kStepThreads, 0, s>>>(p);
+    else decay::decay_step_kernel<__nv_bfloat16><<<grid, decay::kStepThreads, 0, s>>>(p);
+    st = cuda_status(cudaGetLastError(), "decay_step_kernel launch");
+    if (st == VRWKV_OK) set_last_kernel("decay_step_kernel");
+    return st;
+}
+
+}  // extern "C"

@@ -20,6 +20,8 @@ struct LayerNormParams {
     int C;
     float eps;
     int vec;  // 16-byte vectors (C * sizeof(IO) % 16 == 0, aligned pointers)
+    float* mean = nullptr;  // row statistics, kept for the backward pass, or nullptr
+    float* rstd = nullptr;
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -63,6 +65,10 @@ __global__ void __launch_bounds__(256) layer_norm_reg_kernel(const LayerNormPara
         }
     }
     const float rstd = rsqrtf(warp_sum(q) * invC + p.eps);
+    if (p.mean && lane == 0) {
+        p.mean[row] = mean;
+        p.rstd[row] = rstd;
+    }
 #pragma unroll
     for (int k = 0; k < VPL; ++k) {
         const int v = lane + 32 * k;
@@ -112,6 +118,10 @@ __global__ void __launch_bounds__(256) layer_norm_kernel(const LayerNormParams p
             for (int e = 0; e < N; ++e) q = fmaf(f[e] - mean, f[e] - mean, q);
         }
         const float rstd = rsqrtf(warp_sum(q) * invC + p.eps);
+        if (p.mean && lane == 0) {
+            p.mean[row] = mean;
+            p.rstd[row] = rstd;
+        }
         for (int v = lane; v < nv; v += 32) {
             float f[N], o[N];
             V::unpack(*reinterpret_cast<const uint4*>(xr + (size_t)v * 16), f);
@@ -131,6 +141,10 @@ __global__ void __launch_bounds__(256) layer_norm_kernel(const LayerNormParams p
             q = fmaf(d, d, q);
         }
         const float rstd = rsqrtf(warp_sum(q) * invC + p.eps);
+        if (p.mean && lane == 0) {
+            p.mean[row] = mean;
+            p.rstd[row] = rstd;
+        }
         for (int c = lane; c < p.C; c += 32) {
             const float d = Io<IO>::ld1(xr + (size_t)c * sizeof(IO)) - mean;
             Io<IO>::st1(yr + (size_t)c * sizeof(IO), fmaf(__ldg(p.g + c), d * rstd, __ldg(p.b + c)));

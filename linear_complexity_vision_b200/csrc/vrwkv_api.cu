@@ -28,6 +28,7 @@
 #include "biwkv_bwd_tm.cuh"
 #include "layer_norm.cuh"
 #include "gemm_tc.cuh"
+#include "api_internal.h"
 
 // Device error word: set by kernels whose bounded waits ran out (bit 0).
 __device__ unsigned int g_vrwkv_device_error;
@@ -38,6 +39,12 @@ using namespace vrwkv;
 
 thread_local std::string g_last_error;
 thread_local const char* g_last_kernel = "";
+
+}  // namespace
+
+// Host helpers shared with the other translation units (api_internal.h).
+namespace vrwkv {
+namespace api {
 
 vrwkv_status fail(vrwkv_status s, const char* fmt, ...) {
     char buf[512];
@@ -69,6 +76,15 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 int elem_bytes(vrwkv_dtype dt) { return dt == VRWKV_F32 ? 4 : 2; }
 
+void set_last_kernel(const char* name) { g_last_kernel = name; }
+
+}  // namespace api
+}  // namespace vrwkv
+
+namespace {
+
+using namespace vrwkv::api;
+
 // Q-Shift channel-group bounds of the q_shift listing: int(C*gamma*j),
 // j = 1..4, with C*gamma formed first and then multiplied by j, both in
 // double precision (the listing's Python evaluation order), truncated.
@@ -91,20 +107,6 @@ bool bounds_multiple_of(const QsBounds& g, int n) {
 // Shifted channel groups of a Q-Shift mode: all four (eq. 9) or the two
 // row groups (bidirectional shift of sparse inputs).
 int shifted_groups(const vrwkv_qshift_params* qs) { return qs && qs->mode == VRWKV_QSHIFT_BIDIR ? 2 : 4; }
-
-
-// Raise the dynamic shared-memory limit of a kernel once per size needed.
-template <typename K>
-cudaError_t ensure_smem(K kernel, std::atomic<int>& granted, int bytes) {
-    if (bytes <= 48 * 1024 || bytes <= granted.load(std::memory_order_relaxed)) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) {
-        int cur = granted.load();
-        while (bytes > cur && !granted.compare_exchange_weak(cur, bytes)) {
-        }
-    }
-    return e;
-}
 
 struct FusedPlan {
     FusedParams p;
@@ -155,10 +157,10 @@ vrwkv_status dispatch_layout(const FusedPlan& pl, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // TMA fast path
 // ---------------------------------------------------------------------------
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
+
+namespace vrwkv {
+namespace api {
 
 EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
@@ -188,6 +190,11 @@ unsigned int* device_error_word() {
     }
     return addr[dev];
 }
+
+}  // namespace api
+}  // namespace vrwkv
+
+namespace {
 
 // Fixed device workspace of vrwkv_spatial_gate_static, for callers that
 // cannot allocate device memory: it is reserved when the module loads, so a
@@ -219,6 +226,11 @@ bool gemm_single_cta_forced() {
     return e && e[0] == '1';
 }
 
+}  // namespace
+
+namespace vrwkv {
+namespace api {
+
 int sm_count() {
     static int n[64] = {};
     int dev = 0;
@@ -230,6 +242,20 @@ int sm_count() {
     }
     return n[dev];
 }
+
+// The wait limit of every device, for kernels that take it as an argument.
+static std::atomic<unsigned long long> g_wait_ns[64];
+unsigned long long wait_limit_ns() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kDefaultWaitNs;
+    const unsigned long long v = g_wait_ns[dev].load(std::memory_order_relaxed);
+    return v ? v : kDefaultWaitNs;
+}
+
+}  // namespace api
+}  // namespace vrwkv
+
+namespace {
 
 // D (M x N) = X (M x K) * W (K x N), all row-major.  bfloat16: W is first
 // transposed into wt (N x K, the K-major B operand) and the product runs on
@@ -1886,22 +1912,7 @@ vrwkv_status vrwkv_spatial_mix_block(const void* x, const void* w_r, const void*
     lp.rows = M;
     lp.C = C;
     lp.eps = ln_eps;
-    lp.vec = ((size_t)C * es) % 16 == 0;
-    const unsigned blocks = (unsigned)((M + 7) / 8);
-    // 16-byte vectors per lane of the register-resident kernel (0: three-pass)
-    const int vpl = (lp.vec && aligned(ln_gamma, 16) && aligned(ln_beta, 16))
-                        ? (int)(((size_t)C * es / 16 + 31) / 32) : 0;
-    auto launch_ln = [&](auto io) {
-        using IO = decltype(io);
-        if (vpl >= 1 && vpl <= 1) layer_norm_reg_kernel<IO, 1><<<blocks, 256, 0, s>>>(lp);
-        else if (vpl == 2) layer_norm_reg_kernel<IO, 2><<<blocks, 256, 0, s>>>(lp);
-        else if (vpl >= 3 && vpl <= 4) layer_norm_reg_kernel<IO, 4><<<blocks, 256, 0, s>>>(lp);
-        else if (vpl >= 5 && vpl <= 8) layer_norm_reg_kernel<IO, 8><<<blocks, 256, 0, s>>>(lp);
-        else layer_norm_kernel<IO><<<blocks, 256, 0, s>>>(lp);
-    };
-    if (dtype == VRWKV_F32) launch_ln(float{});
-    else launch_ln(__nv_bfloat16{});
-    st = cuda_status(cudaGetLastError(), "layer_norm_kernel launch");
+    st = launch_layer_norm(lp, dtype, s);
     if (st == VRWKV_OK) g_last_kernel = "spatial_mix_block";
     return st;
 }
@@ -2195,7 +2206,12 @@ vrwkv_status vrwkv_set_wait_limit(double seconds) {
     if (!(seconds > 0.0 && seconds <= 60.0))
         return fail(VRWKV_ERR_INVALID_ARG, "wait limit must lie in (0, 60] seconds");
     const unsigned long long ns = (unsigned long long)(seconds * 1e9);
-    return cuda_status(cudaMemcpyToSymbol(fast::g_vrwkv_wait_ns, &ns, sizeof(ns)), "setting the wait limit");
+    const vrwkv_status st = cuda_status(cudaMemcpyToSymbol(fast::g_vrwkv_wait_ns, &ns, sizeof(ns)),
+                                        "setting the wait limit");
+    int dev = 0;
+    if (st == VRWKV_OK && cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64)
+        vrwkv::api::g_wait_ns[dev].store(ns, std::memory_order_relaxed);
+    return st;
 }
 
 vrwkv_status vrwkv_device_status(void) {
@@ -2208,9 +2224,10 @@ vrwkv_status vrwkv_device_status(void) {
     const unsigned int zero = 0;
     e = cudaMemcpy(word, &zero, sizeof(zero), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_status(e, "clearing the device error word");
-    return fail(VRWKV_ERR_TIMEOUT,
+    return fail(v == 16u ? VRWKV_ERR_INVALID_ARG : VRWKV_ERR_TIMEOUT,
                 "kernel-side failure (flags 0x%x: 1 = TMA tile wait ran out, 2 = wait for a column "
-                "peer's record ran out, 4 = workspace not zero-filled)",
+                "peer's record ran out, 4 = workspace not zero-filled, 8 = tensor-core wait ran out, "
+                "16 = state slot out of range or repeated)",
                 v);
 }
 
