@@ -4,9 +4,11 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <cstdlib>
 
 #include "api_internal.h"
 #include "decay_attn.cuh"
+#include "decay_attn_tc.cuh"
 
 namespace {
 
@@ -72,20 +74,34 @@ Cut cut_into(int T, int want) {
 }
 
 // One head's chunks run one after the other; segments let more CTAs than
-// heads work.  As many as fill the SMs once with resident CTAs.
-Cut plan_f32(int B, int T, int H, int D, int nprob) {
-    const int resident = padded_d(D) == 128 ? 1 : 4;
+// heads work.  As many as fill the SMs once with resident CTAs: 4 of 49 KB or
+// 1 of 123 KB on the FP32 pipes, 2 (D = 64) or 1 on the tensor cores.
+Cut plan(int B, int T, int H, int D, int nprob, bool tc) {
+    const int resident = tc ? (D == 64 ? 2 : 1) : (padded_d(D) == 128 ? 1 : 4);
     const long long heads = (long long)B * H * nprob;
     const long long slots = (long long)sm_count() * resident;
     return cut_into(T, (int)std::max<long long>(1, slots / heads));
 }
 
+// The tensor-core kernel takes bfloat16 heads of 64 or 128 channels;
+// VRWKV_DECAY_TC=0 keeps them on the FP32 pipes (diagnostics and tests).
+bool tc_sizes(int D, vrwkv_dtype dtype) {
+    const char* e = getenv("VRWKV_DECAY_TC");
+    return dtype == VRWKV_BF16 && (D == 64 || D == 128) && !(e && e[0] == '0' && e[1] == 0);
+}
+
 size_t state_floats(int B, int H, int D, int nseg) { return (size_t)B * H * nseg * D * D; }
 
+// The larger of what the two kernels' cuts need: which of them runs also
+// depends on the tensors' alignment.
 size_t ws_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
-    const Cut c = plan_f32(B, T, H, D, backward ? 3 : 1);
-    if (c.nseg == 1) return 0;
-    return ((backward ? 2 : 1) * state_floats(B, H, D, c.nseg) * 4 + 255) / 256 * 256;
+    size_t need = 0;
+    for (int tc = 0; tc <= (tc_sizes(D, dtype) ? 1 : 0); ++tc) {
+        const Cut c = plan(B, T, H, D, backward ? 3 : 1, tc != 0);
+        if (c.nseg > 1)
+            need = std::max(need, ((backward ? 2 : 1) * state_floats(B, H, D, c.nseg) * 4 + 255) / 256 * 256);
+    }
+    return need;
 }
 
 // ---- launches ----
@@ -110,8 +126,77 @@ vrwkv_status launch_io(const decay::Params& p, cudaStream_t s) {
     }
 }
 
-vrwkv_status launch_attn(const decay::Params& p, vrwkv_dtype dtype, cudaStream_t s) {
-    return dtype == VRWKV_F32 ? launch_io<float>(p, s) : launch_io<__nv_bfloat16>(p, s);
+// ---- tensor cores ----
+// A token tensor as TMA reads it: (C, T, B) with rows ld elements apart, in
+// boxes of 64 channels x 128 tokens (rows past T arrive as zeros).
+bool encode_tokens(CUtensorMap* m, const void* x, long long ld, int B, int T, int C) {
+    const EncodeTiledFn enc = encode_fn();
+    const cuuint64_t dims[3] = {(cuuint64_t)C, (cuuint64_t)T, (cuuint64_t)B};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)T * ld * 2};
+    const cuuint32_t box[3] = {64, decay::kTcChunk, 1}, estr[3] = {1, 1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool tma_ok(const void* x, long long ld) { return aligned(x, 16) && ld % 8 == 0 && ld < (1LL << 36); }
+
+template <int D, bool OUT>
+vrwkv_status launch_tc_d(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
+    static std::atomic<int> granted{0};
+    constexpr int smem = decay::tc_smem_bytes<D>();
+    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT>, granted, smem);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    decay::decay_attn_tc_kernel<D, OUT><<<ctas, decay::kTcThreads, smem, s>>>(p);
+    return cuda_status(cudaGetLastError(), "decay_attn_tc_kernel launch");
+}
+
+// Launch p's problems; with `tc`, on the tensor cores with its maps.
+struct Launcher {
+    vrwkv_dtype dtype;
+    bool tc;
+    decay::TcParams t;  // maps, error word, wait limit
+    const void* src[4]; // the tensors behind the maps, and their row strides
+    long long ld[4];
+
+    int map_of(const char* x, long long row) const {
+        for (int i = 0; i < 4; ++i)
+            if (src[i] == x && ld[i] == row) return i;
+        return 0;  // no q: the state alone
+    }
+    vrwkv_status run(const decay::Params& p, cudaStream_t s) {
+        if (!tc) return dtype == VRWKV_F32 ? launch_io<float>(p, s) : launch_io<__nv_bfloat16>(p, s);
+        const long long ctas = (long long)p.B * p.H * p.nseg * p.nprob;
+        if (ctas > INT_MAX) return fail(VRWKV_ERR_UNSUPPORTED, "too many heads (B*H = %lld)", (long long)p.B * p.H);
+        t.p = p;
+        for (int i = 0; i < p.nprob; ++i) {
+            t.mq[i] = map_of(p.pr[i].q, p.pr[i].ldq);
+            t.mk[i] = map_of(p.pr[i].k, p.pr[i].ldk);
+            t.mv[i] = map_of(p.pr[i].v, p.pr[i].ldv);
+        }
+        const bool out = p.pr[0].out != nullptr;
+        if (p.D == 64) return out ? launch_tc_d<64, true>(t, (unsigned)ctas, s) : launch_tc_d<64, false>(t, (unsigned)ctas, s);
+        return out ? launch_tc_d<128, true>(t, (unsigned)ctas, s) : launch_tc_d<128, false>(t, (unsigned)ctas, s);
+    }
+};
+
+// The tensor-core kernel where the sizes, alignments and row strides of all
+// n <= 4 tensors allow, else the FP32 pipes.
+Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long* ld, int n, bool outs16, int B, int T,
+                       int H, int D) {
+    Launcher l = {};
+    l.dtype = dtype;
+    l.tc = tc_sizes(D, dtype) && outs16;
+    for (int i = 0; i < n && l.tc; ++i) l.tc = tma_ok(x[i], ld[i]);
+    if (!l.tc) return l;
+    l.t.err = device_error_word();
+    l.t.wait_ns = wait_limit_ns();
+    l.tc = l.t.err != nullptr;
+    for (int i = 0; i < n && l.tc; ++i) {
+        l.src[i] = x[i];
+        l.ld[i] = ld[i];
+        l.tc = encode_tokens(&l.t.map[i], x[i], ld[i], B, T, H * D);
+    }
+    return l;
 }
 
 vrwkv_status launch_chain(const decay::ChainParams& p, int bh, int nprob, cudaStream_t s) {
@@ -157,7 +242,10 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     st = check_overlaps(outs, 3, ins, 6);
     if (st != VRWKV_OK) return st;
 
-    const Cut cut = plan_f32(B, T, H, D, 1);
+    const void* srcs[3] = {q, k, v};
+    const long long lds[3] = {ldq, ldk, ldv};
+    Launcher attn = make_launcher(dtype, srcs, lds, 3, aligned(out, 16), B, T, H, D);
+    const Cut cut = plan(B, T, H, D, 1, attn.tc);
     decay::Params p = {};
     p.w = w;
     p.lengths = lengths;
@@ -182,7 +270,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     float* ws = static_cast<float*>(workspace);
     if (cut.nseg > 1) {
         pr.x_out = ws;
-        st = launch_attn(p, dtype, s);
+        st = attn.run(p, s);
         if (st != VRWKV_OK) return st;
         decay::ChainParams c = {};
         c.pr[0] = {ws, state, state_out, 0};
@@ -202,8 +290,8 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
         pr.x_out = state_out;
     }
     pr.out = static_cast<char*>(out);
-    st = launch_attn(p, dtype, s);
-    if (st == VRWKV_OK) set_last_kernel("decay_attn_kernel");
+    st = attn.run(p, s);
+    if (st == VRWKV_OK) set_last_kernel(attn.tc ? "decay_attn_tc_kernel" : "decay_attn_kernel");
     return st;
 }
 
@@ -237,7 +325,11 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     st = check_overlaps(outs, 5, ins, 8);
     if (st != VRWKV_OK) return st;
 
-    const Cut cut = plan_f32(B, T, H, D, 3);
+    const void* srcs[4] = {q, k, v, gy};
+    const long long lds[4] = {ldq, ldk, ldv, ldg};
+    Launcher attn =
+        make_launcher(dtype, srcs, lds, 4, aligned(gq, 16) && aligned(gk, 16) && aligned(gv, 16), B, T, H, D);
+    const Cut cut = plan(B, T, H, D, 3, attn.tc);
     decay::Params p = {};
     p.w = w;
     p.lengths = lengths;
@@ -276,7 +368,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
         c.scale_upd = scale;
         c.reverse = 1;
         p.nprob = 2;
-        st = launch_attn(p, dtype, s);
+        st = attn.run(p, s);
         if (st != VRWKV_OK) return st;
         decay::ChainParams cp = {};
         cp.pr[0] = {ws, state, nullptr, 0};
@@ -300,8 +392,8 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     // gk: (v, g, q) in reversed time on (dL/dS)^T; gv: (k, q, g) on dL/dS
     p.pr[1] = {V, G, Q, static_cast<char*>(gk), ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale};
     p.pr[2] = {K, Q, G, static_cast<char*>(gv), ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale};
-    st = launch_attn(p, dtype, s);
-    if (st == VRWKV_OK) set_last_kernel("decay_attn_kernel");
+    st = attn.run(p, s);
+    if (st == VRWKV_OK) set_last_kernel(attn.tc ? "decay_attn_tc_kernel" : "decay_attn_kernel");
     return st;
 }
 
