@@ -140,20 +140,26 @@ bool encode_tokens(CUtensorMap* m, const void* x, long long ld, int B, int T, in
 }
 bool tma_ok(const void* x, long long ld) { return aligned(x, 16) && ld % 8 == 0 && ld < (1LL << 36); }
 
-template <int D, bool OUT>
-vrwkv_status launch_tc_d(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
+template <int D, bool OUT, int PIECES>
+vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
     static std::atomic<int> granted{0};
-    constexpr int smem = decay::tc_smem_bytes<D>();
-    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT>, granted, smem);
+    constexpr int smem = decay::tc_smem_bytes<D, OUT>();
+    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT, PIECES>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    decay::decay_attn_tc_kernel<D, OUT><<<ctas, decay::kTcThreads, smem, s>>>(p);
+    decay::decay_attn_tc_kernel<D, OUT, PIECES><<<ctas, decay::tc_threads<D>(), smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_tc_kernel launch");
+}
+template <int D>
+vrwkv_status launch_tc_d(const decay::TcParams& p, bool exact, unsigned ctas, cudaStream_t s) {
+    if (p.p.pr[0].out) return exact ? launch_tc<D, true, 3>(p, ctas, s) : launch_tc<D, true, 2>(p, ctas, s);
+    return exact ? launch_tc<D, false, 3>(p, ctas, s) : launch_tc<D, false, 2>(p, ctas, s);
 }
 
 // Launch p's problems; with `tc`, on the tensor cores with its maps.
 struct Launcher {
     vrwkv_dtype dtype;
     bool tc;
+    bool exact;         // a state leaves the call: three pieces (decay_attn_tc.cuh)
     decay::TcParams t;  // maps, error word, wait limit
     const void* src[4]; // the tensors behind the maps, and their row strides
     long long ld[4];
@@ -173,19 +179,23 @@ struct Launcher {
             t.mk[i] = map_of(p.pr[i].k, p.pr[i].ldk);
             t.mv[i] = map_of(p.pr[i].v, p.pr[i].ldv);
         }
-        const bool out = p.pr[0].out != nullptr;
-        if (p.D == 64) return out ? launch_tc_d<64, true>(t, (unsigned)ctas, s) : launch_tc_d<64, false>(t, (unsigned)ctas, s);
-        return out ? launch_tc_d<128, true>(t, (unsigned)ctas, s) : launch_tc_d<128, false>(t, (unsigned)ctas, s);
+        return p.D == 64 ? launch_tc_d<64>(t, exact, (unsigned)ctas, s) : launch_tc_d<128>(t, exact, (unsigned)ctas, s);
     }
 };
 
 // The tensor-core kernel where the sizes, alignments and row strides of all
 // n <= 4 tensors allow, else the FP32 pipes.
-Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long* ld, int n, bool outs16, int B, int T,
-                       int H, int D) {
+Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long* ld, int n, const void* const* outs,
+                       int no, bool state_leaves, int B, int T, int H, int D) {
     Launcher l = {};
     l.dtype = dtype;
-    l.tc = tc_sizes(D, dtype) && outs16;
+    l.exact = state_leaves;
+    l.tc = tc_sizes(D, dtype);
+    l.t.wide_out = 1;
+    for (int i = 0; i < no; ++i) {
+        l.tc = l.tc && aligned(outs[i], 16);
+        if (!aligned(outs[i], 32)) l.t.wide_out = 0;
+    }
     for (int i = 0; i < n && l.tc; ++i) l.tc = tma_ok(x[i], ld[i]);
     if (!l.tc) return l;
     l.t.err = device_error_word();
@@ -243,8 +253,9 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     if (st != VRWKV_OK) return st;
 
     const void* srcs[3] = {q, k, v};
+    const void* dsts[1] = {out};
     const long long lds[3] = {ldq, ldk, ldv};
-    Launcher attn = make_launcher(dtype, srcs, lds, 3, aligned(out, 16), B, T, H, D);
+    Launcher attn = make_launcher(dtype, srcs, lds, 3, dsts, 1, state_out != nullptr, B, T, H, D);
     const Cut cut = plan(B, T, H, D, 1, attn.tc);
     decay::Params p = {};
     p.w = w;
@@ -326,9 +337,10 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     if (st != VRWKV_OK) return st;
 
     const void* srcs[4] = {q, k, v, gy};
+    const void* dsts[3] = {gq, gk, gv};
     const long long lds[4] = {ldq, ldk, ldv, ldg};
     Launcher attn =
-        make_launcher(dtype, srcs, lds, 4, aligned(gq, 16) && aligned(gk, 16) && aligned(gv, 16), B, T, H, D);
+        make_launcher(dtype, srcs, lds, 4, dsts, 3, gstate_in != nullptr, B, T, H, D);
     const Cut cut = plan(B, T, H, D, 3, attn.tc);
     decay::Params p = {};
     p.w = w;
