@@ -22,14 +22,15 @@
 // so fast decays underflow to 0 instead of overflowing; the diagonal block
 // takes it from a table by t - s.
 //
-// All warps share every step; a warp's quarter of tensor memory (its number
-// mod 4) decides its rows, its warpgroup the columns.  The blocks of P on and
-// below the diagonal fall unevenly on the quarters (1, 2, 3, 4 of 10), so K~
-// is dealt out the other way round.  One lane (thread 0) issues loads and
-// MMAs.  q's tile (and k's, with two pieces) is loaded for the next chunk as
-// soon as its last reader is done.
-// D = 64: 8 warps, 96 KB of tiles, 256 tensor-memory columns, two CTAs per
-// SM, which fill each other's waits.  D = 128: 16 warps, 224 KB, one CTA.
+// All working warps share every step; a warp's quarter of tensor memory (its
+// number mod 4) decides its rows, its warpgroup the columns.  The blocks of P
+// on and below the diagonal fall unevenly on the quarters (1, 2, 3, 4 of 10),
+// so K~ is dealt out the other way round.  One more warp issues loads and
+// MMAs and works on nothing else, since issuing waits for the tensor pipe.
+// q's tile (and k's, with two pieces) is loaded for the next chunk as soon as
+// its last reader is done.
+// D = 64: 8 working warps, 96 KB of tiles, 256 tensor-memory columns, two CTAs
+// per SM, which fill each other's waits.  D = 128: 16 warps, 224 KB, one CTA.
 //
 // Every wait is bounded: a wait that runs out records flag 8 in the device
 // error word, makes every warp leave its loop, waits (bounded) for copies and
@@ -56,7 +57,7 @@ struct TcParams {
 
 template <int D>
 __host__ __device__ constexpr int tc_threads() {
-    return D == 64 ? 256 : 512;
+    return D == 64 ? 288 : 544;  // the last warp issues
 }
 
 // Tiles of a CTA; without outputs neither q nor the state's operands.
@@ -106,17 +107,17 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     decay_attn_tc_kernel(const __grid_constant__ TcParams P) {
     using Sm = TcSmem<D, OUT>;
     constexpr int C = kTcChunk, SUB = Sm::kSub, SUBB = 128 * 128, kThreads = tc_threads<D>();
-    constexpr int NWG = kThreads / 128, NW = kThreads / 32;
+    constexpr int NWG = kThreads / 128, NW = 4 * NWG, kWork = 32 * NW;
     constexpr uint32_t kColO = 128, kColU = OUT ? 128 + D : 0;
     constexpr uint32_t kCols = OUT ? (D == 64 ? 256 : 512) : D;
-    constexpr int NX = D * D / kThreads;                // state values of a thread
+    constexpr int NX = D * D / kWork;                   // state values of a thread
     extern __shared__ __align__(1024) char smem_raw[];
     Sm& S = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
     const Params& p = P.p;
     const int prob = blockIdx.x % p.nprob;
     const Problem& pr = p.pr[prob];
     const int sid = blockIdx.x / p.nprob, seg = sid % p.nseg, bh = sid / p.nseg, b = bh / p.H, h = bh % p.H;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, wg = warp >> 2;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, quad = warp & 3, wg = warp >> 2;
     const float w = __ldg(p.w + h);
     const int n_seq = seq_tokens(p.lengths, b, p.T);
     const int t0 = seg * p.seg_tokens;
@@ -165,24 +166,26 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     // chunk ci of the walk: its first token in the segment
     auto first = [&](int ci) { return (rev ? nchunk - 1 - ci : ci) * C; };
     const uint32_t sq = tc::smem_u32(S.q), sk = tc::smem_u32(S.k), sv = tc::smem_u32(S.v);
+    const uint32_t skh = tc::smem_u32(S.kh), skm = tc::smem_u32(S.km), sxh = tc::smem_u32(S.xh), sxl = tc::smem_u32(S.xl);
     auto load = [&](uint32_t dst, int map, int ci, unsigned long long* bar) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
             tc::tma_load_3d(dst + s * SUBB, &P.map[map], h * D + 64 * s, t0 + first(ci), b, bar);
     };
-    int loads = 0;        // (thread 0) chunks whose loads were begun
-    bool issued = false;  // (thread 0) MMAs were issued
-    auto begin_loads = [&]() {
-        tc::mbar_expect_tx(&S.fa, (OUT ? 2 : 1) * Sm::kTile);
-        tc::mbar_expect_tx(&S.fv, Sm::kTile);
-        ++loads;
-    };
     __syncthreads();
-    if (tid == 0 && nchunk > 0) {
-        begin_loads();
-        load(sk, P.mk[prob], 0, &S.fa);
-        if (OUT) load(sq, P.mq[prob], 0, &S.fa);
-        load(sv, P.mv[prob], 0, &S.fv);
+    const bool issuer = warp == NW;
+    auto load_a = [&](int ci) {
+        tc::mbar_expect_tx(&S.fa, (OUT ? 2 : 1) * Sm::kTile);
+        load(sk, P.mk[prob], ci, &S.fa);
+        if (OUT) load(sq, P.mq[prob], ci, &S.fa);
+    };
+    auto load_v = [&](int ci) {
+        tc::mbar_expect_tx(&S.fv, Sm::kTile);
+        load(sv, P.mv[prob], ci, &S.fv);
+    };
+    if (issuer && nchunk > 0 && tc::elect_one()) {
+        load_a(0);
+        load_v(0);
     }
 
     // X: row jr of X^T (a v channel), columns c0 .. (k channels).  For D = 64
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     const int jr = D == 64 ? (quad & 1) * 32 + lane : quad * 32 + lane;
     const int c0 = D == 64 ? ((quad >> 1) * 2 + wg) * NX : wg * NX;
     float X[NX];
-    if (has_in) {
+    if (has_in && !issuer) {
         const float* x = pr.x_in + xo;
 #pragma unroll
         for (int i = 0; i < NX; ++i)
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         tc::fence_async_smem();
         arrive_warp(S.xr);
     };
-    if (OUT && has_in) store_x();
+    if (OUT && has_in && !issuer) store_x();
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -228,32 +231,124 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     constexpr uint32_t kIdX = tc::idesc_bf16(128, D, false, false);
     constexpr uint32_t kIdP = tc::idesc_bf16(128, D, false, true);
     constexpr uint32_t kIdU = tc::idesc_bf16(128, D, true, true);
+    if (issuer) {
+        int loads_a = 1, loads_v = 1;  // loads begun, if there are tokens
+        bool issued = false;
+        for (int ci = 0; ci < nchunk; ++ci) {
+            const bool more = ci + 1 < nchunk, update = more || has_out, with_x = OUT && (ci > 0 || has_in);
+            const int xphase = ci - (has_in ? 0 : 1);   // of xr and qs
+            if (!wait_warp(S.fa, ci)) break;
+            tc::fence_after();
+            if (OUT) {                                  // A = q k^T
+                issued = true;
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < SUB; ++s) {
+                        const uint64_t da = tc::sw128_desc(sq + s * SUBB, 16), db = tc::sw128_desc(sk + s * SUBB, 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) tc::mma_ss(tmem, da + 2 * k, db + 2 * k, kIdA, s + k > 0);
+                    }
+                    tc::commit(&S.qk);
+                }
+                __syncwarp();
+            }
+            if (with_x) {                               // O = q X
+                if (!wait_warp(S.xr, xphase) || (ci > 0 && !wait_warp(S.of, ci - 1))) break;
+                tc::fence_after();
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int s = 0; s < SUB; ++s) {
+                            const uint64_t da = tc::sw128_desc(sq + s * SUBB, 16);
+                            const uint64_t db = tc::sw128_desc((half ? sxl : sxh) + s * D * 128, 16);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_ss(tmem + kColO, da + 2 * k, db + 2 * k, kIdX, half + s + k > 0);
+                        }
+                    tc::commit(&S.qs);
+                }
+                __syncwarp();
+            }
+            if (!wait_warp(S.kt, ci) || !wait_warp(S.fv, ci)) break;
+            tc::fence_after();
+            if (update) {                               // U = v^T K~
+                issued = true;
+                if (tc::elect_one()) {
+                    const uint64_t da = tc::sw128_desc(sv, D == 64 ? 0 : SUBB);
+#pragma unroll
+                    for (int piece = 0; piece < PIECES; ++piece) {
+                        const uint64_t db = tc::sw128_desc(piece == 0 ? skh : piece == 1 ? skm : sk, SUBB);
+#pragma unroll
+                        for (int k = 0; k < C / 16; ++k)
+                            tc::mma_ss(tmem + kColU, da + 128 * k, db + 128 * k, kIdU, piece + k > 0);
+                    }
+                    tc::commit(&S.u);
+                }
+                __syncwarp();
+            }
+            if (OUT) {                                  // O += P v
+                if (!wait_warp(S.pr, ci)) break;
+                tc::fence_after();
+                if (tc::elect_one()) {
+                    const uint64_t db = tc::sw128_desc(sv, SUBB);
+                    const uint32_t acc = with_x ? 1u : 0u;
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            tc::mma_ts(tmem + kColO, tmem + 16 * k + 8 * half, db + 128 * k, kIdP,
+                                       k + half > 0 ? 1u : acc);
+                    tc::commit(&S.o);
+                }
+                __syncwarp();
+            }
+            if (!more) break;
+            // with P done, A and O = q X have read q's tile, and k's with K~
+            // unless that holds the third piece
+            if (PIECES == 2) {
+                if (tc::elect_one()) load_a(ci + 1);
+                ++loads_a;
+                __syncwarp();
+            }
+            if ((OUT && !wait_warp(S.o, ci)) || !wait_warp(S.u, ci)) break;
+            if (tc::elect_one()) {
+                if (PIECES == 3) load_a(ci + 1);
+                load_v(ci + 1);
+            }
+            if (PIECES == 3) ++loads_a;
+            ++loads_v;
+            __syncwarp();
+        }
+        if (*abort) {
+            // what was begun ends before the CTA's memory is given back
+            const unsigned long long s0 = tc::global_ns();
+            while (nchunk > 0 && !(tc::mbar_test(&S.fa, (unsigned)(loads_a - 1) & 1u) &&
+                                   tc::mbar_test(&S.fv, (unsigned)(loads_v - 1) & 1u)) &&
+                   tc::global_ns() - s0 <= P.wait_ns) {
+            }
+            __syncwarp();
+            if (issued) {
+                if (tc::elect_one()) tc::commit(&S.drain);
+                __syncwarp();
+                while (!tc::mbar_test(&S.drain, 0) && tc::global_ns() - s0 <= 2 * P.wait_ns) {
+                }
+            }
+        }
+        __syncwarp();
+    }
+
     // this warp's 512-byte units of K~ (4 rows of 64 channels): 7, 5, 3, 1 by quarter
     const int wq = rev ? 3 - quad : quad;               // blocks of P off the diagonal in this quarter
     const int units = 7 - 2 * wq, unit0 = NWG * (wq * (8 - wq)) + wg * units;
-
     int ci = 0;
-    for (; ci < nchunk; ++ci) {
+    for (; ci < nchunk && !issuer; ++ci) {
         const int a = first(ci), m = min(C, n - a);
-        const bool update = ci + 1 < nchunk || has_out, with_x = OUT && (ci > 0 || has_in);
-        const bool more = ci + 1 < nchunk;
-        const int xphase = ci - (has_in ? 0 : 1);       // of xr and qs
+        const bool more = ci + 1 < nchunk, update = more || has_out, with_x = OUT && (ci > 0 || has_in);
         if (!wait_warp(S.fa, ci)) break;
-        if (OUT && tid == 0) {                          // A = q k^T
-            tc::fence_after();
-            issued = true;
-#pragma unroll
-            for (int s = 0; s < SUB; ++s) {
-                const uint64_t da = tc::sw128_desc(sq + s * SUBB, 16), db = tc::sw128_desc(sk + s * SUBB, 16);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tc::mma_ss(tmem, da + 2 * k, db + 2 * k, kIdA, s + k > 0);
-            }
-            tc::commit(&S.qk);
-        }
-        __syncwarp();
         if (m < C) {  // rows of v past the chunk's tokens meet zeros of P and K~: 0 * NaN is NaN
             if (!wait_warp(S.fv, ci)) break;
-            for (int x = tid; x < (C - m) * 8 * SUB; x += kThreads)
+            for (int x = tid; x < (C - m) * 8 * SUB; x += kWork)
                 *reinterpret_cast<uint4*>(S.v + (x / ((C - m) * 8)) * SUBB + (m + x % ((C - m) * 8) / 8) * 128 +
                                           (x % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -286,45 +381,10 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         }
         tc::fence_async_smem();
         arrive_warp(S.kt);
-        if (tid == 0) {
-            if (with_x && wait(S.xr, xphase) && (ci == 0 || wait(S.of, ci - 1))) {  // O = q X
-                tc::fence_after();
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int s = 0; s < SUB; ++s) {
-                        const uint64_t da = tc::sw128_desc(sq + s * SUBB, 16);
-                        const uint64_t db = tc::sw128_desc(tc::smem_u32(half ? S.xl : S.xh) + s * D * 128, 16);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma_ss(tmem + kColO, da + 2 * k, db + 2 * k, kIdX, half + s + k > 0);
-                    }
-                tc::commit(&S.qs);
-            }
-            if (update && wait(S.kt, ci) && wait(S.fv, ci)) {  // U = v^T K~
-                tc::fence_after();
-                issued = true;
-                const uint64_t da = tc::sw128_desc(sv, D == 64 ? 0 : SUBB);
-#pragma unroll
-                for (int piece = 0; piece < PIECES; ++piece) {
-                    const uint64_t db =
-                        tc::sw128_desc(piece == 0 ? tc::smem_u32(S.kh) : piece == 1 ? tc::smem_u32(S.km) : sk, SUBB);
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        tc::mma_ss(tmem + kColU, da + 128 * k, db + 128 * k, kIdU, piece + k > 0);
-                }
-                tc::commit(&S.u);
-                if (!OUT && more) {
-                    begin_loads();
-                    if (PIECES == 2) load(sk, P.mk[prob], ci + 1, &S.fa);  // k's tile is read
-                }
-            }
-        }
-        __syncwarp();
         if (OUT) {
             if (!wait_warp(S.qk, ci)) break;
             tc::fence_after();
-            // P: this warpgroup's blocks of the quarter's rows, dj blocks back in (walked) time
+            // P: this warpgroup's blocks of the quarter's rows, d4 blocks back in (walked) time
 #pragma unroll
             for (int jj = 0; jj < 4 / NWG; ++jj) {
                 const int d4 = NWG == 4 ? wg : (wg == 0 ? 3 * jj : 1 + jj);
@@ -333,75 +393,64 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                     tc::tmem_zero32(lanes + 32 * j);
                     continue;
                 }
-                float v[32];
-                tc::tmem_ld32(lanes + 32 * j, v);
-                if (d4 == 0) {
-                    const float* dg = S.diag + 31 - lane;
+                const float2 f = f2(S.pw[d4 == 0 ? 0 : rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);
+                const float* dg = S.diag + 31 - lane;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= dg[i];
-                } else {
-                    const float2 f = f2(S.pw[rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);
+                for (int g = 0; g < 32; g += 16) {      // 16 columns become 8 of hi and 8 of lo
+                    float v[16];
+                    tc::tmem_ld16(lanes + 32 * j + g, v);
+                    if (d4 == 0) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 c = *reinterpret_cast<const float4*>(S.col + i);
-                        const float2 x = mul2(f2(v[i], v[i + 1]), mul2(f2(c.x, c.y), f));
-                        const float2 y = mul2(f2(v[i + 2], v[i + 3]), mul2(f2(c.z, c.w), f));
-                        v[i] = x.x;
-                        v[i + 1] = x.y;
-                        v[i + 2] = y.x;
-                        v[i + 3] = y.y;
+                        for (int i = 0; i < 16; ++i) v[i] *= dg[g + i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 c = *reinterpret_cast<const float4*>(S.col + g + i);
+                            const float2 x = mul2(f2(v[i], v[i + 1]), mul2(f2(c.x, c.y), f));
+                            const float2 y = mul2(f2(v[i + 2], v[i + 3]), mul2(f2(c.z, c.w), f));
+                            v[i] = x.x;
+                            v[i + 1] = x.y;
+                            v[i + 2] = y.x;
+                            v[i + 3] = y.y;
+                        }
                     }
-                }
-                if (32 * j + 32 > m) {  // columns past the chunk's tokens
+                    if (32 * j + g + 16 > m) {          // columns past the chunk's tokens
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * j + i >= m) v[i] = 0.f;
-                }
-                uint32_t out[32];
+                        for (int i = 0; i < 16; ++i)
+                            if (32 * j + g + i >= m) v[i] = 0.f;
+                    }
+                    uint32_t out[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 x = f2(v[2 * i], v[2 * i + 1]);
-                    out[i] = split_bf16(x);
-                    out[16 + i] = pack_bf16(x);
+                    for (int i = 0; i < 8; ++i) {
+                        float2 x = f2(v[2 * i], v[2 * i + 1]);
+                        out[i] = split_bf16(x);
+                        out[8 + i] = pack_bf16(x);
+                    }
+                    tc::tmem_st16(lanes + 32 * j + g, out);
                 }
-                tc::tmem_st32(lanes + 32 * j, out);
             }
             if (with_x) {
-                if (!wait_warp(S.qs, xphase)) break;
+                if (!wait_warp(S.qs, ci - (has_in ? 0 : 1))) break;
                 tc::fence_after();
                 const int row = quad * 32 + lane;
                 const float2 f = f2(S.pw[max(rev ? m - 1 - row : row, 0) + e0] * pr.scale_inter);
-                float v[32];
-                uint32_t out[32];
-                tc::tmem_ld32(lanes + kColO + wg * 32, v);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 x = mul2(f2(v[i], v[i + 1]), f);
-                    out[i] = __float_as_uint(x.x);
-                    out[i + 1] = __float_as_uint(x.y);
+                for (int g = 0; g < 32; g += 16) {
+                    float v[16];
+                    uint32_t out[16];
+                    tc::tmem_ld16(lanes + kColO + wg * 32 + g, v);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 x = mul2(f2(v[i], v[i + 1]), f);
+                        out[i] = __float_as_uint(x.x);
+                        out[i + 1] = __float_as_uint(x.y);
+                    }
+                    tc::tmem_st16(lanes + kColO + wg * 32 + g, out);
                 }
-                tc::tmem_st32(lanes + kColO + wg * 32, out);
             }
             tc::tmem_wait_st();
             tc::fence_before();
             arrive_warp(S.pr);
-            if (tid == 0 && wait(S.pr, ci) && wait(S.kt, ci) && wait(S.fv, ci)) {  // O += P v
-                tc::fence_after();
-                const uint64_t db = tc::sw128_desc(sv, SUBB);
-#pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        tc::mma_ts(tmem + kColO, tmem + 32 * (k / 2) + 16 * half + 8 * (k % 2), db + 128 * k, kIdP,
-                                   with_x || k + half > 0);
-                tc::commit(&S.o);
-                if (more) {  // q's tile is read, and k's unless it holds the third piece
-                    begin_loads();
-                    if (PIECES == 2) load(sk, P.mk[prob], ci + 1, &S.fa);
-                    load(sq, P.mq[prob], ci + 1, &S.fa);
-                }
-            }
-            __syncwarp();
         }
         if (update) {
             if (!wait_warp(S.u, ci)) break;
@@ -418,11 +467,6 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
             }
             tc::fence_before();
             if (OUT && more) store_x();
-            if (tid == 0 && more && (!OUT || wait(S.o, ci))) {  // v's tile is read, and k's third piece
-                if (PIECES == 3) load(sk, P.mk[prob], ci + 1, &S.fa);
-                load(sv, P.mv[prob], ci + 1, &S.fv);
-            }
-            __syncwarp();
         }
         if (OUT) {
             if (!wait_warp(S.o, ci)) break;
@@ -449,7 +493,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
             }
         }
     }
-    if (has_out && ci == nchunk) {
+    if (has_out && !issuer && ci == nchunk) {
         float* x = pr.x_out + xo;
 #pragma unroll
         for (int i = 0; i < NX; ++i) x[pr.x_out_t ? (size_t)jr * D + c0 + i : (size_t)(c0 + i) * D + jr] = X[i];
@@ -458,19 +502,6 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         for (int x = tid; x < (t_end - n) * (D / 8); x += kThreads)
             *reinterpret_cast<uint4*>(pr.out + (((size_t)b * p.T + t0 + n + x / (D / 8)) * p.H + h) * D * 2 +
                                       (x % (D / 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (tid == 0 && *abort) {
-        // what was begun ends before the CTA's memory is given back
-        const unsigned long long s0 = tc::global_ns();
-        while (loads > 0 && !(tc::mbar_test(&S.fa, (unsigned)(loads - 1) & 1u) &&
-                              tc::mbar_test(&S.fv, (unsigned)(loads - 1) & 1u)) &&
-               tc::global_ns() - s0 <= P.wait_ns) {
-        }
-        if (issued) {
-            tc::commit(&S.drain);
-            while (!tc::mbar_test(&S.drain, 0) && tc::global_ns() - s0 <= 2 * P.wait_ns) {
-            }
-        }
     }
     tc::fence_before();
     __syncthreads();
