@@ -23,12 +23,11 @@
 // takes it from a table by t - s.
 //
 // All working warps share every step; a warp's quarter of tensor memory (its
-// number mod 4) decides its rows, its warpgroup the columns.  The blocks of P
-// on and below the diagonal fall unevenly on the quarters (1, 2, 3, 4 of 10),
-// so K~ is dealt out the other way round.  One more warp issues loads and
-// MMAs and works on nothing else, since issuing waits for the tensor pipe.
-// q's tile (and k's, with two pieces) is loaded for the next chunk as soon as
-// its last reader is done.
+// number mod 4) decides its rows, its warpgroup the columns.  One more warp
+// issues loads and MMAs and works on nothing else, since issuing waits for the
+// tensor pipe.  The tiles are loaded for the next chunk as soon as their last
+// readers are done: q and k (unless it holds the third piece) after A, O = q X
+// and K~, a whole chunk's work ahead; v after O += P v.
 // D = 64: 8 working warps, 96 KB of tiles, 256 tensor-memory columns, two CTAs
 // per SM, which fill each other's waits.  D = 128: 16 warps, 224 KB, one CTA.
 //
@@ -72,7 +71,7 @@ struct alignas(1024) TcSmem {
     float pw[kTcChunk + 4];                             // e^{-w n}, n = 0 .. 128
     float diag[64];  // scale_intra e^{-w d}, 0 for d < 0; d = t - s (s - t reversed) at 31 - d (31 + d)
     float col[32];   // scale_intra e^{-w (31-i)}, reversed scale_intra e^{-w i}
-    unsigned long long fa, fv, qk, qs, kt, u, pr, o, xr, of, drain;
+    unsigned long long fa, fv, a, kt, u, pr, o, xr, of, drain;
     unsigned tmem;
     int abort;
 };
@@ -131,8 +130,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     if (tid == 0) {
         tc::mbar_init(&S.fa, 1);
         tc::mbar_init(&S.fv, 1);
-        tc::mbar_init(&S.qk, 1);
-        tc::mbar_init(&S.qs, 1);
+        tc::mbar_init(&S.a, 1);
         tc::mbar_init(&S.kt, NW);
         tc::mbar_init(&S.u, 1);
         tc::mbar_init(&S.pr, NW);
@@ -174,17 +172,18 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     };
     __syncthreads();
     const bool issuer = warp == NW;
-    auto load_a = [&](int ci) {
+    auto load_q = [&](int ci) {  // begins fa's phase; k completes it
         tc::mbar_expect_tx(&S.fa, (OUT ? 2 : 1) * Sm::kTile);
-        load(sk, P.mk[prob], ci, &S.fa);
         if (OUT) load(sq, P.mq[prob], ci, &S.fa);
     };
+    auto load_k = [&](int ci) { load(sk, P.mk[prob], ci, &S.fa); };
     auto load_v = [&](int ci) {
         tc::mbar_expect_tx(&S.fv, Sm::kTile);
         load(sv, P.mv[prob], ci, &S.fv);
     };
     if (issuer && nchunk > 0 && tc::elect_one()) {
-        load_a(0);
+        load_q(0);
+        load_k(0);
         load_v(0);
     }
 
@@ -232,11 +231,10 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     constexpr uint32_t kIdP = tc::idesc_bf16(128, D, false, true);
     constexpr uint32_t kIdU = tc::idesc_bf16(128, D, true, true);
     if (issuer) {
-        int loads_a = 1, loads_v = 1;  // loads begun, if there are tokens
+        int loads_a = 1, loads_v = 1;  // phases of fa and fv begun, if there are tokens
         bool issued = false;
         for (int ci = 0; ci < nchunk; ++ci) {
             const bool more = ci + 1 < nchunk, update = more || has_out, with_x = OUT && (ci > 0 || has_in);
-            const int xphase = ci - (has_in ? 0 : 1);   // of xr and qs
             if (!wait_warp(S.fa, ci)) break;
             tc::fence_after();
             if (OUT) {                                  // A = q k^T
@@ -248,12 +246,12 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) tc::mma_ss(tmem, da + 2 * k, db + 2 * k, kIdA, s + k > 0);
                     }
-                    tc::commit(&S.qk);
+                    if (!with_x) tc::commit(&S.a);
                 }
                 __syncwarp();
             }
             if (with_x) {                               // O = q X
-                if (!wait_warp(S.xr, xphase) || (ci > 0 && !wait_warp(S.of, ci - 1))) break;
+                if (!wait_warp(S.xr, ci - (has_in ? 0 : 1)) || (ci > 0 && !wait_warp(S.of, ci - 1))) break;
                 tc::fence_after();
                 if (tc::elect_one()) {
 #pragma unroll
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                             for (int k = 0; k < 4; ++k)
                                 tc::mma_ss(tmem + kColO, da + 2 * k, db + 2 * k, kIdX, half + s + k > 0);
                         }
-                    tc::commit(&S.qs);
+                    tc::commit(&S.a);
                 }
                 __syncwarp();
             }
@@ -287,6 +285,15 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 }
                 __syncwarp();
             }
+            if (more) {                                 // q's tile is read, and k's or nearly
+                if (OUT && !wait_warp(S.a, ci)) break;
+                if (tc::elect_one()) {
+                    load_q(ci + 1);
+                    if (PIECES == 2) load_k(ci + 1);
+                }
+                ++loads_a;
+                __syncwarp();
+            }
             if (OUT) {                                  // O += P v
                 if (!wait_warp(S.pr, ci)) break;
                 tc::fence_after();
@@ -304,19 +311,11 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 __syncwarp();
             }
             if (!more) break;
-            // with P done, A and O = q X have read q's tile, and k's with K~
-            // unless that holds the third piece
-            if (PIECES == 2) {
-                if (tc::elect_one()) load_a(ci + 1);
-                ++loads_a;
-                __syncwarp();
-            }
             if ((OUT && !wait_warp(S.o, ci)) || !wait_warp(S.u, ci)) break;
             if (tc::elect_one()) {
-                if (PIECES == 3) load_a(ci + 1);
+                if (PIECES == 3) load_k(ci + 1);
                 load_v(ci + 1);
             }
-            if (PIECES == 3) ++loads_a;
             ++loads_v;
             __syncwarp();
         }
@@ -338,9 +337,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         __syncwarp();
     }
 
-    // this warp's 512-byte units of K~ (4 rows of 64 channels): 7, 5, 3, 1 by quarter
     const int wq = rev ? 3 - quad : quad;               // blocks of P off the diagonal in this quarter
-    const int units = 7 - 2 * wq, unit0 = NWG * (wq * (8 - wq)) + wg * units;
     int ci = 0;
     for (; ci < nchunk && !issuer; ++ci) {
         const int a = first(ci), m = min(C, n - a);
@@ -353,15 +350,22 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                                           (x % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         if (update) {
-            if (OUT && PIECES == 3 && !wait_warp(S.qk, ci)) break;  // the third piece takes k's own tile
-#pragma unroll 2
-            for (int i = 0; i < units; ++i) {
-                const int x = (unit0 + i) * 32 + lane, r = (x % 1024) / 8;
-                const uint32_t off = x * 16;
-                const float2 f = f2(S.pw[rev ? r + 1 : max(m - 1 - r, 0)] * pr.scale_upd);
-                uint4 raw = *reinterpret_cast<const uint4*>(S.k + off);
-                if (r >= m) raw = make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+            if (OUT && PIECES == 3 && !wait_warp(S.a, ci)) break;  // the third piece takes k's own tile
+            constexpr int kUnits = 8 * SUB * 128 / kWork;  // 16-byte pieces of a thread
+            uint4 raws[kUnits];
+            float fs[kUnits];
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const int x = i * kWork + tid, r = (x % 1024) / 8;
+                raws[i] = *reinterpret_cast<const uint4*>(S.k + x * 16);
+                fs[i] = S.pw[rev ? r + 1 : max(m - 1 - r, 0)] * pr.scale_upd;
+                if (r >= m) raws[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const uint32_t off = (i * kWork + tid) * 16;
+                const float2 f = f2(fs[i]);
+                const uint32_t rw[4] = {raws[i].x, raws[i].y, raws[i].z, raws[i].w};
                 uint32_t hi[4], mi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         tc::fence_async_smem();
         arrive_warp(S.kt);
         if (OUT) {
-            if (!wait_warp(S.qk, ci)) break;
+            if (!wait_warp(S.a, ci)) break;
             tc::fence_after();
             // P: this warpgroup's blocks of the quarter's rows, d4 blocks back in (walked) time
 #pragma unroll
@@ -395,10 +399,13 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 }
                 const float2 f = f2(S.pw[d4 == 0 ? 0 : rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);
                 const float* dg = S.diag + 31 - lane;
+                float all[32];
+                tc::tmem_ld32(lanes + 32 * j, all);
 #pragma unroll
                 for (int g = 0; g < 32; g += 16) {      // 16 columns become 8 of hi and 8 of lo
                     float v[16];
-                    tc::tmem_ld16(lanes + 32 * j + g, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = all[g + i];
                     if (d4 == 0) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] *= dg[g + i];
@@ -430,8 +437,6 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 }
             }
             if (with_x) {
-                if (!wait_warp(S.qs, ci - (has_in ? 0 : 1))) break;
-                tc::fence_after();
                 const int row = quad * 32 + lane;
                 const float2 f = f2(S.pw[max(rev ? m - 1 - row : row, 0) + e0] * pr.scale_inter);
 #pragma unroll
