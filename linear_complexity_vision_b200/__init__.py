@@ -472,17 +472,18 @@ def biwkv_bwd(k, v, w, u, gy, totals: bool = True, out=None):
     return gk, gv, gw, gu, gwt, gut
 
 
-def _require_rows(name, t, shape, dtype, device) -> int:
+# The calls below serve single tokens, where the host's time counts: their
+# checks read each tensor's attributes once, and the stream and device are
+# asked for directly.
+def _stream_of(device) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _row_stride(name, t, shape) -> int:
     """Row stride in elements of a token tensor whose rows of C channels are
-    evenly spaced: contiguous, or a column slice of a wider tensor."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {tuple(shape)} tensor of {dtype}")
-    C = shape[-1]
-    if t.is_contiguous():
-        return C
-    stride = t.stride()
+    evenly spaced (a column slice of a wider tensor)."""
+    C, stride = shape[-1], t.stride()
     if C > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: the channels of a row must be adjacent")
     # the rows' spacing, from the innermost dimension that has more than one
@@ -501,17 +502,30 @@ def _require_rows(name, t, shape, dtype, device) -> int:
     return ld
 
 
+def _require_rows(name, t, shape, dtype, device) -> int:
+    """Row stride of a CUDA token tensor of this shape, dtype and device."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {tuple(shape)} tensor of {dtype}")
+    return shape[-1] if t.is_contiguous() else _row_stride(name, t, shape)
+
+
+def _require_like(name, t, shape, dtype, device, want) -> None:
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must match {want} in shape, dtype and device, and be contiguous")
+
+
 def _require_f32(name, t, shape, device) -> None:
     import torch
-    _require(t, name)
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or t.device != device:
-        raise ValueError(f"{name} must be a float32 tensor of shape {tuple(shape)} on {device}")
+    if (t.dtype != torch.float32 or t.shape != shape or t.device != device or not t.is_cuda
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a float32 tensor of shape {tuple(shape)} on {device}, contiguous")
 
 
 def _require_ints(name, t, n, device) -> None:
     import torch
-    _require(t, name)
-    if t.dtype != torch.int32 or tuple(t.shape) != (n,) or t.device != device:
+    if t.dtype != torch.int32 or t.shape != (n,) or t.device != device or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be an int32 tensor of {n} elements on {device}")
 
 
@@ -521,25 +535,26 @@ def _ptr(t):
 
 class _on:
     """Make a tensor's device the current one for a call."""
+    __slots__ = ("index", "back")
 
     def __init__(self, device):
-        self.device = device
+        self.index = device.index
 
     def __enter__(self):
         import torch
-        now = torch.cuda.current_device()
-        self.back = now if self.device.index is not None and self.device.index != now else None
-        if self.back is not None:
-            torch.cuda.set_device(self.device)
+        now = torch._C._cuda_getDevice()
+        self.back = None
+        if self.index != now:
+            self.back = now
+            torch.cuda.set_device(self.index)
 
     def __exit__(self, *exc):
-        import torch
         if self.back is not None:
+            import torch
             torch.cuda.set_device(self.back)
 
 
 def _heads(shape, heads: int, what: str) -> int:
-    heads = int(heads)
     if heads <= 0 or shape[-1] % heads != 0:
         raise ValueError(f"{what} must have a whole number of channels for each of {heads} heads")
     return shape[-1] // heads
@@ -547,9 +562,11 @@ def _heads(shape, heads: int, what: str) -> int:
 
 def _workspace(need: int, workspace, device):
     """The caller's workspace, or a new one of `need` bytes (None for 0)."""
-    import torch
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        if not need:
+            return None
+        import torch
+        return torch.empty(need, dtype=torch.uint8, device=device)
     _require(workspace, "workspace")
     if workspace.device != device:
         raise ValueError(f"workspace must be on {device}")
@@ -585,11 +602,12 @@ def decay_attn_fwd(q, k, v, w, heads: int, scale: float = 1.0, state=None, lengt
     import torch
     if q.dim() != 3:
         raise ValueError("q must be a (B, T, C) tensor")
-    B, T, C = q.shape
-    D = _heads(q.shape, heads, "q")
-    dev, code = q.device, _dtype_code(q)
-    ld = [_require_rows(n, t, q.shape, q.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
-    _require_vec(w, heads, dev, "w")
+    shape_q, dtype, dev = q.shape, q.dtype, q.device
+    B, T, C = shape_q
+    D, code = _heads(shape_q, heads, "q"), _dtype_code(q)
+    ldq, ldk, ldv = (_require_rows("q", q, shape_q, dtype, dev), _require_rows("k", k, shape_q, dtype, dev),
+                     _require_rows("v", v, shape_q, dtype, dev))
+    _require_f32("w", w, (heads,), dev)
     shape = (B, heads, D, D)
     for n, t in (("state", state), ("state_out", state_out)):
         if t is not None:
@@ -597,11 +615,9 @@ def decay_attn_fwd(q, k, v, w, heads: int, scale: float = 1.0, state=None, lengt
     if lengths is not None:
         _require_ints("lengths", lengths, B, dev)
     if out is None:
-        out = torch.empty((B, T, C), dtype=q.dtype, device=dev)
+        out = torch.empty(shape_q, dtype=dtype, device=dev)
     else:
-        _require(out, "out")
-        if out.shape != q.shape or out.dtype != q.dtype or out.device != dev:
-            raise ValueError("out must match q in shape, dtype and device")
+        _require_like("out", out, shape_q, dtype, dev, "q")
     if state_out is None and want_state:
         state_out = torch.empty(shape, dtype=torch.float32, device=dev)
     lib = load_library()
@@ -609,8 +625,8 @@ def decay_attn_fwd(q, k, v, w, heads: int, scale: float = 1.0, state=None, lengt
         need = 0 if workspace is not None else int(lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 0))
         ws = _workspace(need, workspace, dev)
         _check(lib.vrwkv_decay_attn_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), *ld, w.data_ptr(), _ptr(state), _ptr(lengths), float(scale),
-            out.data_ptr(), _ptr(state_out), B, T, heads, D, code, *_ws_args(ws), _stream_ptr(q)))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, w.data_ptr(), _ptr(state), _ptr(lengths), scale,
+            out.data_ptr(), _ptr(state_out), B, T, heads, D, code, *_ws_args(ws), _stream_of(dev)))
     return out, state_out
 
 
@@ -624,11 +640,11 @@ def decay_attn_bwd(q, k, v, w, heads: int, gy, scale: float = 1.0, state=None, g
     import torch
     if q.dim() != 3:
         raise ValueError("q must be a (B, T, C) tensor")
-    B, T, C = q.shape
-    D = _heads(q.shape, heads, "q")
-    dev, code = q.device, _dtype_code(q)
-    ld = [_require_rows(n, t, q.shape, q.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v), ("gy", gy))]
-    _require_vec(w, heads, dev, "w")
+    shape_q, dtype, dev = q.shape, q.dtype, q.device
+    B, T, C = shape_q
+    D, code = _heads(shape_q, heads, "q"), _dtype_code(q)
+    ld = [_require_rows(n, t, shape_q, dtype, dev) for n, t in (("q", q), ("k", k), ("v", v), ("gy", gy))]
+    _require_f32("w", w, (heads,), dev)
     shape = (B, heads, D, D)
     if out is None:
         gq, gk, gv = (torch.empty((B, T, C), dtype=q.dtype, device=dev) for _ in range(3))
@@ -636,9 +652,7 @@ def decay_attn_bwd(q, k, v, w, heads: int, gy, scale: float = 1.0, state=None, g
     else:
         gq, gk, gv, gs = out
         for n, t in (("gq", gq), ("gk", gk), ("gv", gv)):
-            _require(t, n)
-            if t.shape != q.shape or t.dtype != q.dtype or t.device != dev:
-                raise ValueError(f"{n} must match q in shape, dtype and device")
+            _require_like(n, t, shape_q, dtype, dev, "q")
     for n, t in (("state", state), ("gstate", gstate), ("gstate_in", gs)):
         if t is not None:
             _require_f32(n, t, shape, dev)
@@ -650,8 +664,8 @@ def decay_attn_bwd(q, k, v, w, heads: int, gy, scale: float = 1.0, state=None, g
         ws = _workspace(need, workspace, dev)
         _check(lib.vrwkv_decay_attn_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), gy.data_ptr(), *ld, w.data_ptr(), _ptr(state), _ptr(gstate),
-            _ptr(lengths), float(scale), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gs), B, T, heads, D, code,
-            *_ws_args(ws), _stream_ptr(q)))
+            _ptr(lengths), scale, gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gs), B, T, heads, D, code,
+            *_ws_args(ws), _stream_of(dev)))
     return gq, gk, gv, gs
 
 
@@ -664,11 +678,12 @@ def decay_attn_step(q, k, v, w, heads: int, state, slots=None, scale: float = 1.
     import torch
     if q.dim() != 2:
         raise ValueError("q must be a (B, C) tensor")
-    B, C = q.shape
-    D = _heads(q.shape, heads, "q")
-    dev, code = q.device, _dtype_code(q)
-    ld = [_require_rows(n, t, q.shape, q.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
-    _require_vec(w, heads, dev, "w")
+    shape_q, dtype, dev = q.shape, q.dtype, q.device
+    B, C = shape_q
+    D, code = _heads(shape_q, heads, "q"), _dtype_code(q)
+    ldq, ldk, ldv = (_require_rows("q", q, shape_q, dtype, dev), _require_rows("k", k, shape_q, dtype, dev),
+                     _require_rows("v", v, shape_q, dtype, dev))
+    _require_f32("w", w, (heads,), dev)
     if state.dim() != 4:
         raise ValueError("state must be a (N, heads, D, D) tensor")
     N = state.shape[0]
@@ -676,15 +691,13 @@ def decay_attn_step(q, k, v, w, heads: int, state, slots=None, scale: float = 1.
     if slots is not None:
         _require_ints("slots", slots, B, dev)
     if out is None:
-        out = torch.empty((B, C), dtype=q.dtype, device=dev)
+        out = torch.empty(shape_q, dtype=dtype, device=dev)
     else:
-        _require(out, "out")
-        if out.shape != q.shape or out.dtype != q.dtype or out.device != dev:
-            raise ValueError("out must match q in shape, dtype and device")
+        _require_like("out", out, shape_q, dtype, dev, "q")
     with _on(dev):
         _check(load_library().vrwkv_decay_attn_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), *ld, w.data_ptr(), state.data_ptr(), _ptr(slots), float(scale),
-            out.data_ptr(), B, N, heads, D, code, _stream_ptr(q)))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, w.data_ptr(), state.data_ptr(), _ptr(slots), scale,
+            out.data_ptr(), B, N, heads, D, code, _stream_of(dev)))
     return out
 
 
@@ -701,21 +714,20 @@ def layer_norm_fwd(x, gamma, beta, eps: float = 1e-5, stats: bool = True, out=No
     mean and rstd (float32, x's shape without C; None without stats)."""
     import torch
     rows, C = _norm_rows(x)
-    dev = x.device
-    for t, name in ((gamma, "gamma"), (beta, "beta")):
-        _require_vec(t, C, dev, name)
+    dev, shape = x.device, x.shape
+    _require_f32("gamma", gamma, (C,), dev)
+    _require_f32("beta", beta, (C,), dev)
     if out is None:
         out = torch.empty_like(x)
     else:
-        _require(out, "out")
-        if out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
-            raise ValueError("out must match x in shape, dtype and device")
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
+        _require_like("out", out, shape, x.dtype, dev, "x")
+    mean = rstd = None
+    if stats:
+        mean, rstd = (torch.empty(shape[:-1], dtype=torch.float32, device=dev) for _ in range(2))
     with _on(dev):
         _check(load_library().vrwkv_layer_norm_fwd(
-            x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), float(eps), out.data_ptr(), _ptr(mean), _ptr(rstd), rows,
-            C, _dtype_code(x), _stream_ptr(x)))
+            x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), eps, out.data_ptr(), _ptr(mean), _ptr(rstd), rows,
+            C, _dtype_code(x), _stream_of(dev)))
     return out, mean, rstd
 
 
@@ -736,18 +748,15 @@ def layer_norm_bwd(x, gamma, mean, rstd, gy, weight_grads: bool = True, out=None
     weight_grads).  out: optional gx to write instead of allocating it."""
     import torch
     rows, C = _norm_rows(x)
-    dev = x.device
-    _require_vec(gamma, C, dev, "gamma")
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _require_vec(t, rows, dev, name)
-    _require(gy, "gy")
+    dev, shape = x.device, x.shape
+    _require_f32("gamma", gamma, (C,), dev)
+    _require_f32("mean", mean, shape[:-1], dev)
+    _require_f32("rstd", rstd, shape[:-1], dev)
+    _require_like("gy", gy, shape, x.dtype, dev, "x")
     if out is None:
         out = torch.empty_like(x)
     else:
-        _require(out, "out")
-    for t, name in ((gy, "gy"), (out, "out")):
-        if t.shape != x.shape or t.dtype != x.dtype or t.device != dev:
-            raise ValueError(f"{name} must match x in shape, dtype and device")
+        _require_like("out", out, shape, x.dtype, dev, "x")
     code = _dtype_code(x)
     ggamma = torch.empty(C, dtype=torch.float32, device=dev) if weight_grads else None
     gbeta = torch.empty(C, dtype=torch.float32, device=dev) if weight_grads else None
@@ -759,7 +768,7 @@ def layer_norm_bwd(x, gamma, mean, rstd, gy, weight_grads: bool = True, out=None
         ws = _workspace(need, workspace, dev)
         _check(lib.vrwkv_layer_norm_bwd(
             x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), gy.data_ptr(), out.data_ptr(),
-            _ptr(ggamma), _ptr(gbeta), rows, C, code, *_ws_args(ws), _stream_ptr(x)))
+            _ptr(ggamma), _ptr(gbeta), rows, C, code, *_ws_args(ws), _stream_of(dev)))
     return out, ggamma, gbeta
 
 

@@ -40,26 +40,29 @@ using namespace vrwkv::api;
 
 constexpr int kLnBwdMaxC = 8192;
 
-// Geometry of the backward pass: threads of a CTA (its rows' vectors, NV of
-// them a thread), rows at a time, CTAs.
+// Geometry of the backward pass: a warp per row (vpl vectors a lane) or, with
+// vpl = 0, a CTA per row (nv vectors a thread); threads of a CTA; CTAs.
 struct LnBwdPlan {
     bool vec;
-    int nv, rb, threads, grid;
+    int vpl, nv, threads, grid;
 };
 
 LnBwdPlan ln_bwd_plan(long long rows, int C, int es, bool vec) {
-    LnBwdPlan pl;
+    LnBwdPlan pl = {};
     pl.vec = vec && ((size_t)C * es) % 16 == 0;
     const int vectors = pl.vec ? C * es / 16 : C;
+    if (pl.vec && (vectors + 31) / 32 * (16 / es) <= 32) {
+        pl.vpl = (vectors + 31) / 32;
+        pl.threads = 32 * kLnBwdWarps;
+        // three CTAs of at most 168 registers a thread stay resident
+        pl.grid = (int)std::min<long long>((rows + kLnBwdWarps - 1) / kLnBwdWarps, 3LL * sm_count());
+        return pl;
+    }
     pl.nv = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 8;
     const int per = (vectors + pl.nv - 1) / pl.nv;
     pl.threads = std::min(1024, (per + 31) / 32 * 32);
-    // four rows of at most 256 threads fit their registers; wider ones, one
-    pl.rb = pl.vec && pl.threads <= 256 ? 4 : 1;
-    // as many CTAs as stay resident with about 64 registers a thread
-    const int resident = std::max(1, 1024 / pl.threads);
-    const long long batches = (rows + pl.rb - 1) / pl.rb;
-    pl.grid = (int)std::min<long long>(batches, (long long)sm_count() * resident);
+    // as many CTAs as stay resident with 64 registers a thread
+    pl.grid = (int)std::min<long long>(rows, (long long)sm_count() * std::max(1, 1024 / pl.threads));
     return pl;
 }
 
@@ -69,17 +72,32 @@ size_t ln_bwd_ws_bytes(long long rows, int C, int es) {
     return ((size_t)g * 2 * C * 4 + 255) / 256 * 256;
 }
 
+template <typename IO, int VPL>
+void launch_ln_bwd_warp(const LayerNormBwdParams& p, const LnBwdPlan& pl, cudaStream_t s) {
+    layer_norm_bwd_warp_kernel<IO, VPL><<<pl.grid, pl.threads, 2 * p.C * 4, s>>>(p);  // at most 8 KB
+}
+
 template <typename IO>
 void launch_ln_bwd(const LayerNormBwdParams& p, const LnBwdPlan& pl, cudaStream_t s) {
+    switch (pl.vpl) {
+    case 1: return launch_ln_bwd_warp<IO, 1>(p, pl, s);
+    case 2: return launch_ln_bwd_warp<IO, 2>(p, pl, s);
+    case 3: return launch_ln_bwd_warp<IO, 3>(p, pl, s);
+    case 4: return launch_ln_bwd_warp<IO, 4>(p, pl, s);
+    default: break;
+    }
+    if constexpr (sizeof(IO) == 4) {  // vectors of 4 channels: up to 8 a lane
+        if (pl.vpl == 5 || pl.vpl == 6) return launch_ln_bwd_warp<IO, 6>(p, pl, s);
+        if (pl.vpl > 6) return launch_ln_bwd_warp<IO, 8>(p, pl, s);
+    }
     if (pl.vec) {
-        if (pl.rb == 4) layer_norm_bwd_kernel<IO, true, 1, 4, 256><<<pl.grid, pl.threads, 0, s>>>(p);
-        else if (pl.nv == 1) layer_norm_bwd_kernel<IO, true, 1, 1, 1024><<<pl.grid, pl.threads, 0, s>>>(p);
+        if (pl.nv == 1) layer_norm_bwd_kernel<IO, true, 1><<<pl.grid, pl.threads, 0, s>>>(p);
         else if constexpr (sizeof(IO) == 4)  // bfloat16 rows of kLnBwdMaxC channels are 1024 vectors
-            layer_norm_bwd_kernel<IO, true, 2, 1, 1024><<<pl.grid, pl.threads, 0, s>>>(p);
+            layer_norm_bwd_kernel<IO, true, 2><<<pl.grid, pl.threads, 0, s>>>(p);
     } else {
-        if (pl.nv == 1) layer_norm_bwd_kernel<IO, false, 1, 1, 1024><<<pl.grid, pl.threads, 0, s>>>(p);
-        else if (pl.nv == 2) layer_norm_bwd_kernel<IO, false, 2, 1, 1024><<<pl.grid, pl.threads, 0, s>>>(p);
-        else layer_norm_bwd_kernel<IO, false, 8, 1, 1024><<<pl.grid, pl.threads, 0, s>>>(p);
+        if (pl.nv == 1) layer_norm_bwd_kernel<IO, false, 1><<<pl.grid, pl.threads, 0, s>>>(p);
+        else if (pl.nv == 2) layer_norm_bwd_kernel<IO, false, 2><<<pl.grid, pl.threads, 0, s>>>(p);
+        else layer_norm_bwd_kernel<IO, false, 8><<<pl.grid, pl.threads, 0, s>>>(p);
     }
 }
 

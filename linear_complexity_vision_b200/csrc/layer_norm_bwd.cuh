@@ -1,10 +1,13 @@
 // LayerNorm backward for sm_100a.  With xh = (x - mean) rstd and d = gamma gy per row:
 //   gx = rstd (d - mean_c(d) - xh mean_c(d xh)),
 //   ggamma = sum_rows gy xh,  gbeta = sum_rows gy.
-// Bound by its bytes (x and gy read, gx written once).  A CTA holds RB whole
-// rows in registers (each thread the same NV vectors of every row, so the
-// columns' sums stay in its registers over all rows it visits), reduces the
-// rows' two sums together, and leaves one partial row of ggamma and gbeta;
+// Bound by its bytes (x and gy read, gx written once).  Rows of at most 32
+// channels a lane go to a warp each (layer_norm_bwd_warp_kernel): a row's two
+// sums then cost 10 shuffles and no barrier, and the next row is on its way
+// while one is worked on.  Wider rows, or rows that are not made of aligned
+// 16-byte vectors, go to a CTA each.  Either way a thread keeps the same
+// channels of every row it visits, so their ggamma and gbeta stay in its
+// registers; each CTA leaves one partial row of them, and
 // layer_norm_wgrad_kernel adds the partial rows in a fixed order.
 #pragma once
 
@@ -41,11 +44,107 @@ struct LnVec {
     }
 };
 
-template <typename IO, bool VEC, int NV, int RB, int MAXT>
-__global__ void __launch_bounds__(MAXT) layer_norm_bwd_kernel(const LayerNormBwdParams p) {
+constexpr int kLnBwdWarps = 4;
+
+template <typename IO, int VPL>
+__global__ void __launch_bounds__(32 * kLnBwdWarps, 3) layer_norm_bwd_warp_kernel(const LayerNormBwdParams p) {
+    using V = Vec16<IO>;
+    constexpr int N = V::N, E = VPL * N;  // channels of a lane: vectors lane + 32 k
+    extern __shared__ __align__(16) float sg[];  // gamma, then the CTA's partial rows: max(1, 2) * C floats
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nv = p.C / N;
+    for (int c = tid; c < p.C; c += 32 * kLnBwdWarps) sg[c] = __ldg(p.g + c);
+    __syncthreads();
+    float dg[E], db[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) dg[e] = db[e] = 0.f;
+    const float invC = 1.0f / (float)p.C;
+    const size_t rowb = (size_t)p.C * sizeof(IO);
+    const long long step = (long long)gridDim.x * kLnBwdWarps;
+    long long row = (long long)blockIdx.x * kLnBwdWarps + warp;
+    uint4 nx[VPL], ng[VPL];
+    float nmean = 0.f, nrs = 0.f;
+    auto fetch = [&](long long r) {
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + 32 * k;
+            nx[k] = ng[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (v < nv) {
+                nx[k] = __ldcs(reinterpret_cast<const uint4*>(p.x + r * rowb) + v);
+                ng[k] = __ldcs(reinterpret_cast<const uint4*>(p.gy + r * rowb) + v);
+            }
+        }
+        nmean = __ldg(p.mean + r);
+        nrs = __ldg(p.rstd + r);
+    };
+    if (row < p.rows) fetch(row);
+    for (; row < p.rows; row += step) {
+        uint4 cx[VPL], cg[VPL];
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            cx[k] = nx[k];
+            cg[k] = ng[k];
+        }
+        const float mean = nmean, rs = nrs;
+        if (row + step < p.rows) fetch(row + step);
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + 32 * k;
+            float x[N], y[N];
+            V::unpack(cx[k], x);
+            V::unpack(cg[k], y);
+            if (v >= nv) continue;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float xh = (x[e] - mean) * rs, d = sg[v * N + e] * y[e];
+                a += d;
+                b = fmaf(d, xh, b);
+                dg[k * N + e] = fmaf(y[e], xh, dg[k * N + e]);
+                db[k * N + e] += y[e];
+            }
+        }
+        a = warp_sum(a) * invC;
+        b = warp_sum(b) * invC;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + 32 * k;
+            if (v >= nv) continue;
+            float x[N], y[N], o[N];
+            V::unpack(cx[k], x);
+            V::unpack(cg[k], y);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                o[e] = rs * (fmaf(sg[v * N + e], y[e], -a) - (x[e] - mean) * rs * b);
+            reinterpret_cast<uint4*>(p.gx + row * rowb)[v] = V::pack(o);
+        }
+    }
+    if (!p.part) return;
+    // the warps' sums, in order of the warps
+    for (int w = 0; w < kLnBwdWarps; ++w) {
+        __syncthreads();
+        if (warp != w) continue;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + 32 * k;
+            if (v >= nv) continue;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int c = v * N + e;
+                sg[c] = dg[k * N + e] + (w ? sg[c] : 0.f);
+                sg[p.C + c] = db[k * N + e] + (w ? sg[p.C + c] : 0.f);
+            }
+        }
+    }
+    __syncthreads();
+    for (int c = tid; c < 2 * p.C; c += 32 * kLnBwdWarps) p.part[(size_t)blockIdx.x * 2 * p.C + c] = sg[c];
+}
+
+template <typename IO, bool VEC, int NV>
+__global__ void __launch_bounds__(1024) layer_norm_bwd_kernel(const LayerNormBwdParams p) {
     using V = LnVec<IO, VEC>;
     constexpr int N = V::N;
-    __shared__ float red[2][32][2 * RB];
+    __shared__ float red[2][32][2];
     const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
     const int nv = p.C / N;
     const float invC = 1.0f / (float)p.C;
@@ -59,66 +158,54 @@ __global__ void __launch_bounds__(MAXT) layer_norm_bwd_kernel(const LayerNormBwd
             dg[k][e] = db[k][e] = 0.f;
         }
     int buf = 0;
-    for (long long r0 = (long long)blockIdx.x * RB; r0 < p.rows; r0 += (long long)gridDim.x * RB, buf ^= 1) {
-        float xh[RB][NV][N], gy[RB][NV][N], rs[RB], s[2 * RB];
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buf ^= 1) {
+        float xh[NV][N], gy[NV][N];
+        const float rs = __ldg(p.rstd + row), mean = __ldg(p.mean + row);
+        float a = 0.f, b = 0.f;
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+        for (int k = 0; k < NV; ++k) {
+            const int v = tid + nt * k;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int v = tid + nt * k;
+            for (int e = 0; e < N; ++e) xh[k][e] = gy[k][e] = 0.f;
+            if (v >= nv) continue;
+            const size_t o = ((size_t)row * p.C + (size_t)v * N) * sizeof(IO);
+            V::load(p.x + o, xh[k]);
+            V::load(p.gy + o, gy[k]);
 #pragma unroll
-                for (int e = 0; e < N; ++e) xh[r][k][e] = gy[r][k][e] = 0.f;
-                if (r0 + r < p.rows && v < nv) {
-                    const size_t o = ((size_t)(r0 + r) * p.C + (size_t)v * N) * sizeof(IO);
-                    V::load(p.x + o, xh[r][k]);
-                    V::load(p.gy + o, gy[r][k]);
-                }
+            for (int e = 0; e < N; ++e) {
+                xh[k][e] = (xh[k][e] - mean) * rs;
+                const float d = g[k][e] * gy[k][e];
+                a += d;
+                b = fmaf(d, xh[k][e], b);
+                dg[k][e] = fmaf(gy[k][e], xh[k][e], dg[k][e]);
+                db[k][e] += gy[k][e];
             }
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            const bool live = r0 + r < p.rows;
-            rs[r] = live ? __ldg(p.rstd + r0 + r) : 0.f;
-            const float mean = live ? __ldg(p.mean + r0 + r) : 0.f;
-            float a = 0.f, b = 0.f;
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    xh[r][k][e] = (xh[r][k][e] - mean) * rs[r];
-                    const float d = g[k][e] * gy[r][k][e];
-                    a += d;
-                    b = fmaf(d, xh[r][k][e], b);
-                    dg[k][e] = fmaf(gy[r][k][e], xh[r][k][e], dg[k][e]);
-                    db[k][e] += gy[r][k][e];
-                }
-            s[2 * r] = warp_sum(a);
-            s[2 * r + 1] = warp_sum(b);
         }
+        a = warp_sum(a);
+        b = warp_sum(b);
         if (nw > 1) {
-            // two buffers: the next rows' sums cannot overtake this row's readers
-            if (lane == 0)
-#pragma unroll
-                for (int i = 0; i < 2 * RB; ++i) red[buf][warp][i] = s[i];
+            // two buffers: the next row's sums cannot overtake this row's readers
+            if (lane == 0) {
+                red[buf][warp][0] = a;
+                red[buf][warp][1] = b;
+            }
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 2 * RB; ++i) {
-                s[i] = 0.f;
-                for (int q = 0; q < nw; ++q) s[i] += red[buf][q][i];
+            a = b = 0.f;
+            for (int q = 0; q < nw; ++q) {
+                a += red[buf][q][0];
+                b += red[buf][q][1];
             }
         }
+        a *= invC;
+        b *= invC;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            if (r0 + r >= p.rows) break;
-            const float a = s[2 * r] * invC, b = s[2 * r + 1] * invC;
+        for (int k = 0; k < NV; ++k) {
+            const int v = tid + nt * k;
+            if (v >= nv) continue;
+            float o[N];
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int v = tid + nt * k;
-                if (v >= nv) continue;
-                float o[N];
-#pragma unroll
-                for (int e = 0; e < N; ++e) o[e] = rs[r] * (fmaf(g[k][e], gy[r][k][e], -a) - xh[r][k][e] * b);
-                V::store(p.gx + ((size_t)(r0 + r) * p.C + (size_t)v * N) * sizeof(IO), o);
-            }
+            for (int e = 0; e < N; ++e) o[e] = rs * (fmaf(g[k][e], gy[k][e], -a) - xh[k][e] * b);
+            V::store(p.gx + ((size_t)row * p.C + (size_t)v * N) * sizeof(IO), o);
         }
     }
     if (!p.part) return;
@@ -143,8 +230,10 @@ __global__ void __launch_bounds__(1024) layer_norm_wgrad_kernel(const float* par
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (c < 2 * C)
+    if (c < 2 * C) {
+#pragma unroll 8
         for (int i = warp; i < n; i += 32) s += part[(size_t)i * 2 * C + c];
+    }
     sm[warp][lane] = s;
     __syncthreads();
     const float t = warp_sum(sm[lane][warp]);  // column warp of the CTA's 32
