@@ -9,6 +9,7 @@
 #include "api_internal.h"
 #include "decay_attn.cuh"
 #include "decay_attn_tc.cuh"
+#include "decay_attn_tc64.cuh"
 
 namespace {
 
@@ -77,10 +78,11 @@ Cut cut_into(int T, int want) {
 // heads work.  As many as fill the SMs once with resident CTAs: 4 of 49 KB or
 // 1 of 123 KB on the FP32 pipes, 2 (D = 64) or 1 on the tensor cores.
 Cut plan(int B, int T, int H, int D, int nprob, bool tc) {
-    const int resident = tc ? (D == 64 ? 2 : 1) : (padded_d(D) == 128 ? 1 : 4);
+    const int resident = tc ? 1 : (padded_d(D) == 128 ? 1 : 4);
     const long long heads = (long long)B * H * nprob;
     const long long slots = (long long)sm_count() * resident;
-    return cut_into(T, (int)std::max<long long>(1, slots / heads));
+    const int units = (T + kSegUnit - 1) / kSegUnit;
+    return cut_into(T, (int)std::max<long long>(1, std::min<long long>(slots / heads, units / 2)));
 }
 
 // The tensor-core kernel takes bfloat16 heads of 64 or 128 channels;
@@ -149,10 +151,22 @@ vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, cudaStream_t s) 
     decay::decay_attn_tc_kernel<D, OUT, PIECES><<<ctas, decay::tc_threads<D>(), smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_tc_kernel launch");
 }
-template <int D>
-vrwkv_status launch_tc_d(const decay::TcParams& p, bool exact, unsigned ctas, cudaStream_t s) {
-    if (p.p.pr[0].out) return exact ? launch_tc<D, true, 3>(p, ctas, s) : launch_tc<D, true, 2>(p, ctas, s);
-    return exact ? launch_tc<D, false, 3>(p, ctas, s) : launch_tc<D, false, 2>(p, ctas, s);
+template <int PIECES>
+vrwkv_status launch_tc64(const decay::TcParams& p, cudaStream_t s) {
+    static std::atomic<int> granted{0};
+    constexpr int smem = decay::t64_smem_bytes();
+    const cudaError_t e = ensure_smem(decay::decay_attn_tc64_kernel<PIECES>, granted, smem);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    const unsigned ctas = (unsigned)std::min(p.nitems, sm_count());
+    decay::decay_attn_tc64_kernel<PIECES><<<ctas, decay::kT64Threads, smem, s>>>(p);
+    return cuda_status(cudaGetLastError(), "decay_attn_tc64_kernel launch");
+}
+vrwkv_status launch_tc_any(const decay::TcParams& p, bool exact, cudaStream_t s) {
+    const unsigned n = (unsigned)p.nitems;
+    if (p.p.pr[0].out && p.p.D == 64) return exact ? launch_tc64<3>(p, s) : launch_tc64<2>(p, s);
+    if (p.p.pr[0].out) return exact ? launch_tc<128, true, 3>(p, n, s) : launch_tc<128, true, 2>(p, n, s);
+    if (p.p.D == 64) return exact ? launch_tc<64, false, 3>(p, n, s) : launch_tc<64, false, 2>(p, n, s);
+    return exact ? launch_tc<128, false, 3>(p, n, s) : launch_tc<128, false, 2>(p, n, s);
 }
 
 // Launch p's problems; with `tc`, on the tensor cores with its maps.
@@ -179,7 +193,8 @@ struct Launcher {
             t.mk[i] = map_of(p.pr[i].k, p.pr[i].ldk);
             t.mv[i] = map_of(p.pr[i].v, p.pr[i].ldv);
         }
-        return p.D == 64 ? launch_tc_d<64>(t, exact, (unsigned)ctas, s) : launch_tc_d<128>(t, exact, (unsigned)ctas, s);
+        t.nitems = (int)ctas;
+        return launch_tc_any(t, exact, s);
     }
 };
 
@@ -193,7 +208,7 @@ Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long*
     l.tc = tc_sizes(D, dtype);
     l.t.wide_out = 1;
     for (int i = 0; i < no; ++i) {
-        l.tc = l.tc && aligned(outs[i], 16);
+        l.tc = l.tc && aligned(outs[i], 16) && (D != 64 || encode_tokens(&l.t.omap[i], outs[i], H * D, B, T, H * D));
         if (!aligned(outs[i], 32)) l.t.wide_out = 0;
     }
     for (int i = 0; i < n && l.tc; ++i) l.tc = tma_ok(x[i], ld[i]);
@@ -302,7 +317,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     }
     pr.out = static_cast<char*>(out);
     st = attn.run(p, s);
-    if (st == VRWKV_OK) set_last_kernel(attn.tc ? "decay_attn_tc_kernel" : "decay_attn_kernel");
+    if (st == VRWKV_OK) set_last_kernel(!attn.tc ? "decay_attn_kernel" : D == 64 ? "decay_attn_tc64_kernel" : "decay_attn_tc_kernel");
     return st;
 }
 
@@ -405,7 +420,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     p.pr[1] = {V, G, Q, static_cast<char*>(gk), ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale};
     p.pr[2] = {K, Q, G, static_cast<char*>(gv), ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale};
     st = attn.run(p, s);
-    if (st == VRWKV_OK) set_last_kernel(attn.tc ? "decay_attn_tc_kernel" : "decay_attn_kernel");
+    if (st == VRWKV_OK) set_last_kernel(!attn.tc ? "decay_attn_kernel" : D == 64 ? "decay_attn_tc64_kernel" : "decay_attn_tc_kernel");
     return st;
 }
 

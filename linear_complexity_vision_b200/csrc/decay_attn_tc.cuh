@@ -47,9 +47,11 @@ constexpr unsigned kTcErr = 8u;
 
 struct TcParams {
     CUtensorMap map[4];      // (C, T, B) tensors: box (64, 128, 1), 128-byte swizzle
+    CUtensorMap omap[3];     // the problems' outputs, likewise
     Params p;
     int mq[3], mk[3], mv[3]; // maps of the problems' q, k, v
     int wide_out;            // outputs are 32-byte aligned
+    int nitems;              // CTAs, or work items of the persistent kernel
     unsigned int* err;
     unsigned long long wait_ns;
 };

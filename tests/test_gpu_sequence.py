@@ -142,7 +142,7 @@ CASES = [
 
 
 def _kernel(dt, D):
-    return "decay_attn_tc_kernel" if dt == "bf16" and D in (64, 128) else "decay_attn_kernel"
+    return {64: "decay_attn_tc64_kernel", 128: "decay_attn_tc_kernel"}.get(D if dt == "bf16" else 0, "decay_attn_kernel")
 
 
 @pytest.mark.parametrize("dt,B,T,H,D,packed,state,lens", CASES)
@@ -188,6 +188,22 @@ def test_fp32_pipes_on_tensor_core_sizes(vk, monkeypatch):
         assert vk.load_library().vrwkv_last_kernel() == b"decay_attn_kernel"
         p.check_bwd(p.bwd(vk))
         monkeypatch.delenv("VRWKV_DECAY_TC")
+
+
+@pytest.mark.parametrize("B,T,H,state,ragged", [(60, 150, 7, False, False), (40, 196, 5, True, True), (90, 20, 4, True, True),
+                                                (25, 300, 8, False, True)])
+def test_more_heads_than_sms(vk, B, T, H, state, ragged):
+    """Several heads per persistent CTA, each head with a decay of its own on
+    either side of the fast path's bound, sequences of any number of blocks."""
+    lens = [int(x) for x in np.random.default_rng(16).integers(0, T + 1, B)] if ragged else None
+    p = Problem("bf16", B, T, H, 64, 17, True, state, lens, w=np.exp(np.linspace(-6, 1, H)))
+    out, last = p.fwd(vk)
+    vk.device_status()
+    p.check_fwd(out, last)
+    p.check_fwd(p.fwd(vk, want_state=False)[0], None)
+    got = p.bwd(vk)
+    vk.device_status()
+    p.check_bwd(got)
 
 
 @pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 40)])
