@@ -59,11 +59,24 @@ __device__ __forceinline__ int seg_count(int n, int seg, int seg_tokens) {
     return r < 0 ? 0 : (r > seg_tokens ? seg_tokens : r);
 }
 
-// e^{-w n}.  The exponent is formed in double and rounded once: its absolute
-// error, and so the relative error of the power, stays below |w n| 2^-24.
-__device__ __forceinline__ float decay_pow(float w, int n) {
-    return n == 0 ? 1.0f : exp2f((float)((double)w * (double)n * -1.4426950408889634));
+// e^{-w n} as 2^{n c}, c = -w log2 e held as a float pair: the exponent is
+// rounded once, so the relative error of the power stays below |w n| 2^-24.
+struct DecayBase {
+    float hi, lo;
+};
+__device__ __forceinline__ DecayBase decay_base(float w) {
+    constexpr float L = 1.44269502162933349609375f, Llo = 1.92596299112661748e-8f;  // log2 e = L + Llo
+    DecayBase c;
+    c.hi = -w * L;
+    c.lo = fmaf(-w, L, -c.hi) - w * Llo;
+    return c;
 }
+__device__ __forceinline__ float decay_pow(const DecayBase& c, int n) {
+    if (n == 0) return 1.0f;
+    const float f = (float)n, x = f * c.hi;
+    return exp2f(fabsf(x) < 1e30f ? x + (fmaf(f, c.hi, -x) + f * c.lo) : x);  // an infinite w has no low part
+}
+__device__ __forceinline__ float decay_pow(float w, int n) { return decay_pow(decay_base(w), n); }
 
 template <typename IO>
 __device__ __forceinline__ float4 ld4(const char* p) {

@@ -151,19 +151,37 @@ vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, cudaStream_t s) 
     decay::decay_attn_tc_kernel<D, OUT, PIECES><<<ctas, decay::tc_threads<D>(), smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_tc_kernel launch");
 }
-template <int PIECES>
-vrwkv_status launch_tc64(const decay::TcParams& p, cudaStream_t s) {
+template <int PIECES, int PP>
+vrwkv_status launch_tc64(decay::TcParams& p, cudaStream_t s) {
     static std::atomic<int> granted{0};
     constexpr int smem = decay::t64_smem_bytes();
-    const cudaError_t e = ensure_smem(decay::decay_attn_tc64_kernel<PIECES>, granted, smem);
+    const cudaError_t e = ensure_smem(decay::decay_attn_tc64_kernel<PIECES, PP>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
     const unsigned ctas = (unsigned)std::min(p.nitems, sm_count());
-    decay::decay_attn_tc64_kernel<PIECES><<<ctas, decay::kT64Threads, smem, s>>>(p);
+    int left = (int)ctas;
+    const int radix[3] = {p.p.nprob, p.p.nseg, p.p.H};
+    for (int i = 0; i < 3; ++i) {
+        p.step[i] = left % radix[i];
+        left /= radix[i];
+    }
+    p.step[3] = left;
+    decay::decay_attn_tc64_kernel<PIECES, PP><<<ctas, decay::kT64Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_tc64_kernel launch");
 }
-vrwkv_status launch_tc_any(const decay::TcParams& p, bool exact, cudaStream_t s) {
+// Operands of the tensor cores as one bfloat16 each (P, K~) from this many
+// (sequence, token, head) rows on.  Their roundings, half a step each and
+// independent, then add to the output's own in quadrature: 1.41 times the
+// error of the rounded output (measured 1.41 to 1.42).  Over few rows a single
+// product's rounding could stand out, and time is latency: two pieces, 1.00.
+constexpr long long kRoundedRows = 8192;
+
+vrwkv_status launch_tc_any(decay::TcParams& p, bool exact, cudaStream_t s) {
     const unsigned n = (unsigned)p.nitems;
-    if (p.p.pr[0].out && p.p.D == 64) return exact ? launch_tc64<3>(p, s) : launch_tc64<2>(p, s);
+    const bool rounded = (long long)p.p.B * p.p.T * p.p.H >= kRoundedRows;
+    if (p.p.pr[0].out && p.p.D == 64) {
+        if (rounded) return exact ? launch_tc64<3, 1>(p, s) : launch_tc64<1, 1>(p, s);
+        return exact ? launch_tc64<3, 2>(p, s) : launch_tc64<2, 2>(p, s);
+    }
     if (p.p.pr[0].out) return exact ? launch_tc<128, true, 3>(p, n, s) : launch_tc<128, true, 2>(p, n, s);
     if (p.p.D == 64) return exact ? launch_tc<64, false, 3>(p, n, s) : launch_tc<64, false, 2>(p, n, s);
     return exact ? launch_tc<128, false, 3>(p, n, s) : launch_tc<128, false, 2>(p, n, s);

@@ -52,6 +52,7 @@ struct TcParams {
     int mq[3], mk[3], mv[3]; // maps of the problems' q, k, v
     int wide_out;            // outputs are 32-byte aligned
     int nitems;              // CTAs, or work items of the persistent kernel
+    int step[4];             // its CTAs' stride in items, as (problem, segment, head, sequence)
     unsigned int* err;
     unsigned long long wait_ns;
 };
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 const int d4 = NWG == 4 ? wg : (wg == 0 ? 3 * jj : 1 + jj);
                 const int j = rev ? (quad + d4) & 3 : (quad - d4) & 3;
                 if (d4 > wq || 32 * j >= m) {           // before the sequence's start, or past the chunk's end
-                    tc::tmem_zero32(lanes + 32 * j);
+                    tc::tmem_zero<32>(lanes + 32 * j);
                     continue;
                 }
                 const float2 f = f2(S.pw[d4 == 0 ? 0 : rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);

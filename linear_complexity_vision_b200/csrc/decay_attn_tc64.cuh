@@ -5,7 +5,7 @@
 // warps, an issuing warp), and walks all its work items, one head's segment
 // after the other, without a break: the next item's tiles are loaded and its
 // first chunk begins while the last one's is finished.  Only the state X is
-// serial: two warps keep it in registers, add each chunk's U in turn and hand
+// serial: four warps keep it in registers, add each chunk's U in turn and hand
 // the operands of O = q X to the stream whose chunk is next.
 //
 // Decays.  Where |w| <= 1/2, e^{-w (t - s)} = e^{-w (t - 63)} e^{-w (63 - s)}
@@ -16,8 +16,8 @@
 // 1e24 are safe.)  Faster decays take the block-wise factors of
 // decay_attn_tc.cuh and scale O = q X by rows in tensor memory.
 //
-// Roles (640 threads): warps 0-7 and 8-15 the workers of streams 0 and 1,
-// warps 16-17 the state, warps 18-19 the issuers.  512 tensor-memory columns:
+// Roles (704 threads): warps 0-7 and 8-15 the workers of streams 0 and 1,
+// warps 16-19 the state, warps 20-21 the issuers.  512 tensor-memory columns:
 // per stream A / P 128, O 64, U 64.  Bounded waits as in decay_attn_tc.cuh.
 //
 // A barrier is waited for by its phase's parity, so no phase may complete
@@ -32,7 +32,7 @@
 namespace vrwkv {
 namespace decay {
 
-constexpr int kT64Threads = 640;
+constexpr int kT64Threads = 704;
 constexpr float kT64FastW = 0.5f;
 
 struct alignas(1024) T64Smem {
@@ -58,40 +58,70 @@ constexpr int t64_smem_bytes() { return (int)sizeof(T64Smem) + 1024; }
 
 // A work item: one head's segment of one problem.
 struct T64Item {
-    int prob, b, h, t0, n, nchunk, rev, has_in, has_out;
-    long long xo;
+    int prob, seg, h, b;  // its number's digits, the problem fastest
+    int t0, n, nchunk, rev, has_in, has_out;
+    float w;
+    __device__ __forceinline__ void at(const TcParams& P, int item) {
+        const Params& p = P.p;
+        prob = item % p.nprob;
+        item /= p.nprob;
+        seg = item % p.nseg;
+        item /= p.nseg;
+        h = item % p.H;
+        b = item / p.H;
+        fill(P);
+    }
+    // gridDim.x items on: digit by digit, without divisions
+    __device__ __forceinline__ void step(const TcParams& P) {
+        const Params& p = P.p;
+        prob += P.step[0];
+        seg += P.step[1];
+        h += P.step[2];
+        b += P.step[3];
+        if (prob >= p.nprob) prob -= p.nprob, ++seg;
+        if (seg >= p.nseg) seg -= p.nseg, ++h;
+        if (h >= p.H) h -= p.H, ++b;
+        if (b < p.B) fill(P);
+    }
+    __device__ __forceinline__ void fill(const TcParams& P) {
+        const Params& p = P.p;
+        w = __ldg(p.w + h);
+        t0 = seg * p.seg_tokens;
+        n = seg_count(seq_tokens(p.lengths, b, p.T), seg, p.seg_tokens);
+        nchunk = (n + kTcChunk - 1) / kTcChunk;
+        const Problem& pr = p.pr[prob];
+        rev = pr.reverse;
+        has_in = pr.x_in != nullptr;
+        has_out = pr.x_out != nullptr;
+    }
+    __device__ __forceinline__ long long state_at(const Params& p) const {
+        return (((long long)b * p.H + h) * p.nseg + seg) * 64 * 64;
+    }
+    __device__ __forceinline__ bool fast() const { return fabsf(w) <= kT64FastW; }
 };
-
-__device__ __forceinline__ T64Item t64_item(const TcParams& P, int item) {
-    const Params& p = P.p;
-    T64Item it;
-    it.prob = item % p.nprob;
-    const int sid = item / p.nprob, seg = sid % p.nseg, bh = sid / p.nseg;
-    it.b = bh / p.H;
-    it.h = bh % p.H;
-    it.t0 = seg * p.seg_tokens;
-    it.n = seg_count(seq_tokens(p.lengths, it.b, p.T), seg, p.seg_tokens);
-    it.nchunk = (it.n + kTcChunk - 1) / kTcChunk;
-    const Problem& pr = p.pr[it.prob];
-    it.rev = pr.reverse;
-    it.has_in = pr.x_in != nullptr;
-    it.has_out = pr.x_out != nullptr;
-    it.xo = (long long)(bh * (long long)p.nseg + seg) * 64 * 64;
-    return it;
-}
 
 // A stream's walk over its chunks: every second one of the items' chunks in
 // a row.
 struct T64Cursor {
     int item, ci;
     T64Item it;
+    __device__ __forceinline__ void start(const TcParams& P, int nitems, int stream) {
+        item = blockIdx.x;
+        ci = stream;
+        it.at(P, item);
+        settle(P, nitems);
+    }
+    __device__ __forceinline__ void next(const TcParams& P, int nitems) {
+        ci += 2;
+        settle(P, nitems);
+    }
     __device__ __forceinline__ bool valid(int nitems) const { return item < nitems; }
     __device__ __forceinline__ void settle(const TcParams& P, int nitems) {
         while (ci >= it.nchunk) {
             ci -= it.nchunk;
             item += gridDim.x;
             if (item >= nitems) return;
-            it = t64_item(P, item);
+            it.step(P);
         }
     }
     __device__ __forceinline__ int first() const { return (it.rev ? it.nchunk - 1 - ci : ci) * kTcChunk; }
@@ -101,7 +131,7 @@ struct T64Cursor {
     __device__ __forceinline__ bool with_x() const { return ci > 0 || it.has_in; }
 };
 
-template <int PIECES>
+template <int PIECES, int PP>
 __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const __grid_constant__ TcParams P) {
     constexpr int C = kTcChunk, D = 64;
     extern __shared__ __align__(1024) char smem_raw[];
@@ -119,9 +149,9 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         tc::mbar_init(&B.u, 1);
         tc::mbar_init(&B.pr, 8);
         tc::mbar_init(&B.o, 1);
-        tc::mbar_init(&B.xr, 2);
+        tc::mbar_init(&B.xr, 4);
         tc::mbar_init(&B.of, 8);
-        tc::mbar_init(&B.uf, 2);
+        tc::mbar_init(&B.uf, 4);
         tc::mbar_init(&B.tb, 8);
         tc::mbar_init(&B.qs, 1);
         tc::mbar_init(&B.qk, 1);
@@ -154,24 +184,19 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         constexpr uint32_t kColO = 128;
         int tables_of = -1, turn = 0;                   // item whose tables are built, and how many were
         T64Cursor cu;
-        cu.item = blockIdx.x;
-        cu.ci = s;
-        if (cu.item < nitems) {
-            cu.it = t64_item(P, cu.item);
-            cu.settle(P, nitems);
-        }
+        cu.start(P, nitems, s);
         for (int ph = 0; cu.valid(nitems); ++ph) {      // ph: chunks of this stream so far
             const T64Item& it = cu.it;
             const Problem& pr = p.pr[it.prob];
-            const float w = __ldg(p.w + it.h);
-            const bool fast = fabsf(w) <= kT64FastW;
-            const int rev = it.rev, a = cu.first(), m = cu.tokens();
+            const bool fast = it.fast();
+            const int rev = it.rev, m = cu.tokens();
             const bool update = cu.update();
             if (tables_of != cu.item) {
                 // the other buffer: its last readers are past the barrier of the tables in use
                 ++turn;
                 tables_of = cu.item;
                 T64Smem::Tables& N = S.tab[s][turn & 1];
+                const DecayBase w = decay_base(it.w);
                 if (wt <= C) N.pw[wt] = decay_pow(w, wt);
                 if (wt < C) {
                     if (fast) {
@@ -222,12 +247,12 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                         if (PIECES == 3) {
                             mi[e] = split_bf16(y);
                             lo[e] = pack_bf16(y);
-                        } else {
+                        } else if (PIECES == 2) {
                             mi[e] = pack_bf16(y);
                         }
                     }
                     *reinterpret_cast<uint4*>(T.kh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(T.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                    if (PIECES >= 2) *reinterpret_cast<uint4*>(T.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
                     if (PIECES == 3) *reinterpret_cast<uint4*>(T.k + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
@@ -242,7 +267,8 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 const int d4 = wg == 0 ? 3 * jj : 1 + jj;
                 const int j = rev ? (quad + d4) & 3 : (quad - d4) & 3;
                 if (d4 > wq || 32 * j >= m) {           // before the sequence's start, or past the chunk's end
-                    tc::tmem_zero32(lanes + 32 * j);
+                    if (PP == 2) tc::tmem_zero<32>(lanes + 32 * j);
+                    else tc::tmem_zero<16>(lanes + 32 * j);
                     continue;
                 }
                 float all[32];
@@ -250,6 +276,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 const float2 f = f2(fast ? 1.0f : N.pw[d4 == 0 ? 0 : rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);
                 const float* dg = N.row + 31 - lane;
                 const float* cl = fast ? N.col + 32 * j : N.col;
+                [[maybe_unused]] uint32_t packed[16];
 #pragma unroll
                 for (int g = 0; g < 32; g += 16) {      // 16 columns become 8 of hi and 8 of lo
                     float v[16];
@@ -284,15 +311,21 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                         for (int i = 0; i < 16; ++i)
                             if (32 * j + g + i >= m) v[i] = 0.f;
                     }
-                    uint32_t out[16];
+                    if constexpr (PP == 2) {
+                        uint32_t out[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 x = f2(v[2 * i], v[2 * i + 1]);
-                        out[i] = split_bf16(x);
-                        out[8 + i] = pack_bf16(x);
+                        for (int i = 0; i < 8; ++i) {
+                            float2 x = f2(v[2 * i], v[2 * i + 1]);
+                            out[i] = split_bf16(x);
+                            out[8 + i] = pack_bf16(x);
+                        }
+                        tc::tmem_st16(lanes + 32 * j + g, out);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) packed[g / 2 + i] = pack_bf16(f2(v[2 * i], v[2 * i + 1]));
                     }
-                    tc::tmem_st16(lanes + 32 * j + g, out);
                 }
+                if constexpr (PP == 1) tc::tmem_st16(lanes + 32 * j, packed);
             }
             const int row = quad * 32 + lane;
             if (!fast && cu.with_x()) {
@@ -335,13 +368,13 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
             }
             tc::fence_async_smem();
             arrive(B.so);
-            cu.ci += 2;
-            cu.settle(P, nitems);
+            cu.next(P, nitems);
         }
         // whole blocks of rows past the sequences' ends
         if (p.lengths) {
-            for (int item = blockIdx.x; item < nitems; item += gridDim.x) {
-                const T64Item it = t64_item(P, item);
+            T64Item it;
+            it.at(P, blockIdx.x);
+            for (int item = blockIdx.x; item < nitems; item += gridDim.x, it.step(P)) {
                 const int r0 = it.nchunk * C, rows = min(p.seg_tokens, p.T - it.t0) - r0;
                 for (int x = tid; x < rows * 8; x += 512)
                     *reinterpret_cast<uint4*>(p.pr[it.prob].out +
@@ -349,25 +382,28 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                                               (x % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
         }
-    } else if (warp < 18) {
-        // ---- the state: thread = row of X^T (v channel) ----
-        const int jr = (warp & 1) * 32 + lane;
-        const uint32_t lanes = S.tmem + ((uint32_t)((warp & 1) * 32) << 16);
+    } else if (warp < 20) {
+        // ---- the state: thread = half a row of X^T (v channel jr, k channels c0 ..); U has its rows twice ----
+        constexpr int NX = 32;
+        const int quad = warp & 3, jr = (quad & 1) * 32 + lane, c0 = (quad >> 1) * NX;
+        const uint32_t lanes = S.tmem + ((uint32_t)(quad * 32) << 16) + 192 + c0;
         int g = 0;                                       // chunks so far
         int uphase[2] = {0, 0}, qphase[2] = {0, 0}, last = -1;  // last: stream of the operand stored
         bool okay = true;
-        for (int item = blockIdx.x; item < nitems && okay; item += gridDim.x) {
-            const T64Item it = t64_item(P, item);
+        T64Item it;
+        it.at(P, blockIdx.x);
+        for (int item = blockIdx.x; item < nitems && okay; item += gridDim.x, it.step(P)) {
             const Problem& pr = p.pr[it.prob];
-            const float w = __ldg(p.w + it.h);
-            const bool fast = fabsf(w) <= kT64FastW;
-            float X[D];
+            const DecayBase w = decay_base(it.w);
+            const bool fast = it.fast();
+            const long long xo = it.state_at(p);
+            float X[NX];
             if (it.has_in) {
-                const float* x = pr.x_in + it.xo;
+                const float* x = pr.x_in + xo;
                 if (pr.x_in_t) {
 #pragma unroll
-                    for (int i = 0; i < D; i += 4) {
-                        const float4 y = __ldg(reinterpret_cast<const float4*>(x + jr * D + i));
+                    for (int i = 0; i < NX; i += 4) {
+                        const float4 y = __ldg(reinterpret_cast<const float4*>(x + jr * D + c0 + i));
                         X[i] = y.x;
                         X[i + 1] = y.y;
                         X[i + 2] = y.z;
@@ -375,19 +411,19 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < D; ++i) X[i] = __ldg(x + i * D + jr);
+                    for (int i = 0; i < NX; ++i) X[i] = __ldg(x + (c0 + i) * D + jr);
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < D; ++i) X[i] = 0.f;
+                for (int i = 0; i < NX; ++i) X[i] = 0.f;
             }
             const float full = decay_pow(w, C);
             // X^T as the operand of a chunk of m tokens: row jr, 16-byte piece c at piece c ^ (jr & 7)
             auto store_x = [&](int m, int stream) {
                 const float2 f = f2(fast ? decay_pow(w, it.rev ? m - 64 : 64) * pr.scale_inter : 1.0f);
 #pragma unroll
-                for (int i = 0; i < D; i += 8) {
-                    const uint32_t off = jr * 128 + (((i / 8) ^ (jr & 7)) << 4);
+                for (int i = 0; i < NX; i += 8) {
+                    const uint32_t off = jr * 128 + ((((c0 + i) / 8) ^ (jr & 7)) << 4);
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -421,16 +457,13 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                     if (!okay) break;
                     tc::fence_after();
                     const float2 fx = f2(m == C ? full : decay_pow(w, m));
+                    float v[NX];
+                    tc::tmem_ld32(lanes + s * 256, v);
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        float v[32];
-                        tc::tmem_ld32(lanes + s * 256 + 192 + c, v);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float2 x = fma2(fx, f2(X[c + i], X[c + i + 1]), f2(v[i], v[i + 1]));
-                            X[c + i] = x.x;
-                            X[c + i + 1] = x.y;
-                        }
+                    for (int i = 0; i < NX; i += 2) {
+                        const float2 x = fma2(fx, f2(X[i], X[i + 1]), f2(v[i], v[i + 1]));
+                        X[i] = x.x;
+                        X[i + 1] = x.y;
                     }
                     tc::fence_before();
                     arrive(S.bar[s].uf);
@@ -439,14 +472,14 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 if (!okay) break;
             }
             if (it.has_out && okay) {
-                float* x = pr.x_out + it.xo;
+                float* x = pr.x_out + xo;
 #pragma unroll
-                for (int i = 0; i < D; ++i) x[pr.x_out_t ? jr * D + i : i * D + jr] = X[i];
+                for (int i = 0; i < NX; ++i) x[pr.x_out_t ? jr * D + c0 + i : (c0 + i) * D + jr] = X[i];
             }
         }
     } else {
         // ---- issuer of a stream ----
-        const int s = warp - 18;
+        const int s = warp - 20;
         T64Smem::Stream& T = S.st[s];
         T64Smem::Bars& B = S.bar[s];
         const uint32_t tmem = S.tmem + (uint32_t)(s * 256);
@@ -472,12 +505,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         int loads_a = 0, loads_v = 0, xphase = 0, uphase = 0;
         bool issued = false;
         T64Cursor cu, nx;
-        cu.item = blockIdx.x;
-        cu.ci = s;
-        if (cu.item < nitems) {
-            cu.it = t64_item(P, cu.item);
-            cu.settle(P, nitems);
-        }
+        cu.start(P, nitems, s);
         if (cu.valid(nitems)) {
             if (tc::elect_one()) {
                 load_q(cu);
@@ -489,8 +517,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         }
         for (int ph = 0; cu.valid(nitems); ++ph) {
             nx = cu;
-            nx.ci += 2;
-            nx.settle(P, nitems);
+            nx.next(P, nitems);
             const bool next = nx.valid(nitems), update = cu.update(), with_x = cu.with_x();
             if (!wait(B.fa, ph)) break;
             tc::fence_after();
@@ -553,7 +580,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 if (!wait(B.a, ph)) break;
                 if (tc::elect_one()) {
                     load_q(nx);
-                    if (PIECES == 2) load_k(nx);
+                    if (PIECES < 3) load_k(nx);
                 }
                 ++loads_a;
                 __syncwarp();
@@ -566,8 +593,9 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        tc::mma_ts(tmem + 128, tmem + 16 * k + 8 * half, db + 128 * k, kIdP, k + half > 0 ? 1u : acc);
+                    for (int half = 0; half < PP; ++half)
+                        tc::mma_ts(tmem + 128, tmem + (PP == 2 ? 16 * k + 8 * half : 32 * (k / 2) + 8 * (k % 2)),
+                                   db + 128 * k, kIdP, k + half > 0 ? 1u : acc);
                 tc::tma_store_wait(false);              // the output tile is free
                 tc::commit(&B.o);
             }

@@ -179,10 +179,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
-// 32 columns of zeros.
-__device__ __forceinline__ void tmem_zero32(uint32_t taddr) {
+// N columns of zeros.
+template <int N>
+__device__ __forceinline__ void tmem_zero(uint32_t taddr) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
+    for (int i = 0; i < N; i += 8)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr + i),
                      "r"(0)
                      : "memory");

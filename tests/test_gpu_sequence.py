@@ -11,7 +11,12 @@ terms).  bfloat16 operands: the weighted products q.k, the state and (where no
 state is an output) the decayed keys enter the tensor cores as two bfloat16
 values each.  The first leaves less than 2^-8 of the value, half a step of
 which is at most 2^-17: 1.5 * 2^-16 A for the three, below the 2 * 2^-16 A
-allowed.  The decays'
+allowed.  From 8192 (sequence, token, head) rows on, the products and the keys
+enter as one value each, off by half a step: 2^-8 A for either, 2 * 2^-8 A for
+both.  There the error as a whole is held tighter: roundings independent of
+one another add in quadrature, so its 2-norm stays below 1.5 > sqrt(2) times
+that of the output's own rounding (which an output made of exact products has).
+The decays'
 powers add |w n| u, at most 104 u before they vanish in float32.  The output's
 own rounding is half a step: 2^-8 (bfloat16) of the value.
 """
@@ -53,19 +58,26 @@ def _np(t):
     return t.detach().double().cpu().numpy()
 
 
-def _check(name, got, want, mag, dt, n, lossy=True):
-    """|got - want| <= half a step of the type + n u mag (+ the operand splits)."""
+def _check(name, got, want, mag, dt, n, lossy=True, rounded=False):
+    """|got - want| <= half a step of the type + n u mag (+ the operands' types)."""
     got = _np(got)
     assert np.isfinite(got).all(), name
     step = 2.0 ** -8 if dt == "bf16" else U
-    split = 2 * 2.0 ** -16 if dt == "bf16" and lossy else 0.0
+    split = 2 * (2.0 ** -8 if rounded else 2.0 ** -16) if dt == "bf16" and lossy else 0.0
     tol = step * np.abs(want) + (n * U + split) * mag + 1e-37
     bad = np.abs(got - want) > tol
     assert not bad.any(), (name, int(bad.sum()), float(np.max(np.abs(got - want) / tol)))
+    if rounded:
+        import torch
+        own = _np(torch.from_numpy(want).to(torch.bfloat16)) - want
+        assert np.linalg.norm(got - want) <= 1.5 * np.linalg.norm(own), name
 
 
 def _ops(D, T):
     return 2 * (2 * D + 128 + T) + 16 + 104
+
+
+TC_SIZES = (64,)
 
 
 class Problem:
@@ -81,9 +93,10 @@ class Problem:
         else:
             (self.q, self.qd), (self.k, self.kd), (self.v, self.vd) = (_dev(r.normal(size=(B, T, C)), dt) for _ in range(3))
         self.g, self.gd = _dev(r.normal(size=(B, T, C)), dt)
-        self.w, self.wd = _dev(np.exp(r.uniform(-6, 0.5, H)) if w is None else np.broadcast_to(np.asarray(w, float), (H,)))
+        self.w, self.wd = _dev(np.exp(r.uniform(-6, 0.5, H)) if w is None else np.full(H, w, float))
         self.s, self.sd = _dev(r.normal(size=(B, H, D, D)) if state else None)
         self.gs, self.gsd = _dev(r.normal(size=(B, H, D, D)) if state else None)
+        self.rounded = dt == "bf16" and D in TC_SIZES and B * T * H >= 8192
         self.lens = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
         self.lensd = lens
 
@@ -96,7 +109,7 @@ class Problem:
     def check_fwd(self, out, last):
         want, S, mag, M = seq.decay_attn(self.qd, self.kd, self.vd, self.wd, self.H, self.scale, self.sd, self.lensd)
         n = _ops(self.D, self.T)
-        _check("out", out, want, mag, self.dt, n)
+        _check("out", out, want, mag, self.dt, n, rounded=self.rounded)
         if last is not None:
             _check("state", last, S, M, "f32", n)
 
@@ -104,7 +117,7 @@ class Problem:
         want, mag = seq.decay_attn_bwd(self.qd, self.kd, self.vd, self.wd, self.H, self.gd, self.scale, self.sd, self.gsd, self.lensd)
         n = _ops(self.D, self.T)
         for i, name in enumerate(("gq", "gk", "gv")):
-            _check(name, got[i], want[i], mag[i], self.dt, n)
+            _check(name, got[i], want[i], mag[i], self.dt, n, rounded=self.rounded)
         if got[3] is not None:
             _check("gstate", got[3], want[3], mag[3], "f32", n)
 
