@@ -45,7 +45,7 @@ struct alignas(1024) T64Smem {
         uint8_t q[16384], k[16384], v[16384], kh[16384], km[16384];
         uint8_t out[16384];          // the rows of O on their way out
     } st[2];
-    uint8_t xh[8192], xl[8192];      // X^T as operands of the next chunk
+    uint8_t x[16384];                // X^T as operands of the next chunk, hi and lo; with one piece of K~ km of its stream
     Tables tab[2][2];                // [stream][item's turn]
     struct Bars {
         unsigned long long fa, fv, a, kt, u, pr, o, xr, of, uf, tb, qs, so, qk, drain;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 uint4 raws[4];
                 float fs[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i) {  // 16-byte pieces of a thread
                     const int x = i * 256 + wt, r = x / 8;
                     raws[i] = *reinterpret_cast<const uint4*>(T.k + x * 16);
                     fs[i] = N.pw[rev ? r + 1 : max(m - 1 - r, 0)] * pr.scale_upd;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                             v[i + 2] = y.x;
                             v[i + 3] = y.y;
                         }
-                        if (d4 == 0) {
+                        if (d4 == 0 && PP == 2) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 if (rev ? g + i < lane : g + i > lane) v[i] = 0.f;
@@ -325,7 +325,16 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                         for (int i = 0; i < 8; ++i) packed[g / 2 + i] = pack_bf16(f2(v[2 * i], v[2 * i + 1]));
                     }
                 }
-                if constexpr (PP == 1) tc::tmem_st16(lanes + 32 * j, packed);
+                if constexpr (PP == 1) {
+                    if (d4 == 0 && fast) {              // bits of the columns in the row's future
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int past = rev ? 2 * i + 1 - lane : lane - 2 * i;  // >= 1: both stay, 0: the nearer
+                            packed[i] &= past > 0 ? 0xffffffffu : past < 0 ? 0u : rev ? 0xffff0000u : 0x0000ffffu;
+                        }
+                    }
+                    tc::tmem_st16(lanes + 32 * j, packed);
+                }
             }
             const int row = quad * 32 + lane;
             if (!fast && cu.with_x()) {
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         const int quad = warp & 3, jr = (quad & 1) * 32 + lane, c0 = (quad >> 1) * NX;
         const uint32_t lanes = S.tmem + ((uint32_t)(quad * 32) << 16) + 192 + c0;
         int g = 0;                                       // chunks so far
-        int uphase[2] = {0, 0}, qphase[2] = {0, 0}, last = -1;  // last: stream of the operand stored
+        int uphase[2] = {0, 0}, stored[2] = {0, 0}, last = 0;  // operands stored, the stream of the last
         bool okay = true;
         T64Item it;
         it.at(P, blockIdx.x);
@@ -431,17 +440,22 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                         hi[e] = split_bf16(x);
                         lo[e] = pack_bf16(x);
                     }
-                    *reinterpret_cast<uint4*>(S.xh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(S.xl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    uint8_t* xo = PIECES == 1 ? S.st[stream].km : S.x;
+                    *reinterpret_cast<uint4*>(xo + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(xo + 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 tc::fence_async_smem();
                 arrive(S.bar[stream].xr);
             };
-            // the last O = q X has read the operand (a barrier of its own: a may
-            // be a chunk without X ahead)
+            // after the last O = q X has read the buffer (a barrier of its own: a
+            // may be a chunk without X ahead)
             auto next_x = [&](int m, int stream) {
-                if (last >= 0 && !wait(S.bar[last].qs, qphase[last]++)) return false;
+                const int from = PIECES == 1 ? stream : last;
+                if (stored[stream] + stored[stream ^ 1] > 0 && (PIECES > 1 || stored[stream] > 0) &&
+                    !wait(S.bar[from].qs, stored[from] - 1))
+                    return false;
                 store_x(m, stream);
+                ++stored[stream];
                 last = stream;
                 return true;
             };
@@ -489,7 +503,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         constexpr uint32_t kIdU = tc::idesc_bf16(128, D, true, true);
         const uint32_t sq = tc::smem_u32(T.q), sk = tc::smem_u32(T.k), sv = tc::smem_u32(T.v);
         const uint32_t skh = tc::smem_u32(T.kh), skm = tc::smem_u32(T.km);
-        const uint32_t sxh = tc::smem_u32(S.xh), sxl = tc::smem_u32(S.xl), sout = tc::smem_u32(T.out);
+        const uint32_t sxh = PIECES == 1 ? skm : tc::smem_u32(S.x), sxl = sxh + 8192, sout = tc::smem_u32(T.out);
         auto load = [&](uint32_t dst, int map, const T64Cursor& c, unsigned long long* bar) {
             tc::tma_load_3d(dst, &P.map[map], c.it.h * D, c.it.t0 + c.first(), c.it.b, bar);
         };
@@ -515,6 +529,16 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
             __syncwarp();
             loads_a = loads_v = 1;
         }
+        // the finished chunk's output tile; the lane that begins stores also waits for them
+        int out_map = 0, out_c = 0, out_t = 0, out_b = 0, out_ph = -1;
+        auto store_out = [&]() {
+            if (out_ph < 0) return true;
+            if (!wait(B.so, out_ph)) return false;
+            if (tc::elect_one()) tc::tma_store_3d(&P.omap[out_map], sout, out_c, out_t, out_b);
+            __syncwarp();
+            out_ph = -1;
+            return true;
+        };
         for (int ph = 0; cu.valid(nitems); ++ph) {
             nx = cu;
             nx.next(P, nitems);
@@ -546,14 +570,22 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 }
                 __syncwarp();
             };
-            // U does not wait for X: whichever is ready first goes first
+            auto x_ready = [&]() {
+                return __all_sync(0xffffffffu, tc::mbar_ready(&B.xr, (unsigned)xphase & 1u) ? 1 : 0) != 0;
+            };
+            // U does not wait for X: what is ready first goes first
             if (ph > 0 && !wait(B.of, ph - 1)) break;   // O's columns are read
+            if (!store_out()) break;
             bool x_due = with_x;
-            if (x_due && __all_sync(0xffffffffu, tc::mbar_ready(&B.xr, (unsigned)xphase & 1u) ? 1 : 0)) {
+            if (x_due && x_ready()) {
                 issue_x();
                 x_due = false;
             }
             if (!wait(B.kt, ph) || !wait(B.fv, ph)) break;
+            if (x_due && x_ready()) {
+                issue_x();
+                x_due = false;
+            }
             if (update) {                               // U = v^T K~
                 if (uphase > 0 && !wait(B.uf, uphase - 1)) break;
                 ++uphase;
@@ -611,12 +643,14 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 ++loads_v;
                 __syncwarp();
             }
-            if (!wait(B.so, ph)) break;
-            if (tc::elect_one())                        // the lane that also waits for its stores
-                tc::tma_store_3d(&P.omap[cu.it.prob], sout, cu.it.h * D, cu.it.t0 + cu.first(), cu.it.b);
-            __syncwarp();
+            out_map = cu.it.prob;
+            out_c = cu.it.h * D;
+            out_t = cu.it.t0 + cu.first();
+            out_b = cu.it.b;
+            out_ph = ph;
             cu = nx;
         }
+        store_out();
         if (tc::elect_one()) tc::tma_store_wait(true);
         __syncwarp();
         if (*abort) {
