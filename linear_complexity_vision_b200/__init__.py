@@ -472,12 +472,18 @@ def biwkv_bwd(k, v, w, u, gy, totals: bool = True, out=None):
     return gk, gv, gw, gu, gwt, gut
 
 
-# The calls below serve single tokens, where the host's time counts: their
-# checks read each tensor's attributes once, and the stream and device are
-# asked for directly.
-def _stream_of(device) -> int:
+# The calls below serve single tokens, where the host's time counts: each
+# tensor's attributes are read once, the stream and the device are asked for
+# directly, and what a size needs of workspace is remembered by the size.
+_torch = None
+_ws_need = {}
+
+
+def _load_torch():
+    global _torch
     import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    _torch = torch
+    return torch
 
 
 def _row_stride(name, t, shape) -> int:
@@ -503,55 +509,45 @@ def _row_stride(name, t, shape) -> int:
 
 
 def _require_rows(name, t, shape, dtype, device) -> int:
-    """Row stride of a CUDA token tensor of this shape, dtype and device."""
-    if not t.is_cuda or t.device != device:
+    """Row stride of a token tensor of this shape, dtype and device."""
+    if t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.shape != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be a {tuple(shape)} tensor of {dtype}")
     return shape[-1] if t.is_contiguous() else _row_stride(name, t, shape)
 
 
 def _require_like(name, t, shape, dtype, device, want) -> None:
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must match {want} in shape, dtype and device, and be contiguous")
 
 
 def _require_f32(name, t, shape, device) -> None:
-    import torch
-    if (t.dtype != torch.float32 or t.shape != shape or t.device != device or not t.is_cuda
-            or not t.is_contiguous()):
+    if t.shape != shape or t.dtype is not _torch.float32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a float32 tensor of shape {tuple(shape)} on {device}, contiguous")
 
 
 def _require_ints(name, t, n, device) -> None:
-    import torch
-    if t.dtype != torch.int32 or t.shape != (n,) or t.device != device or not t.is_cuda or not t.is_contiguous():
+    if t.shape != (n,) or t.dtype is not _torch.int32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be an int32 tensor of {n} elements on {device}")
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _tokens_of(name, t, dims: int):
+    """Shape, dtype, device and dtype code of a call's first token tensor."""
+    shape, dtype, device = t.shape, t.dtype, t.device
+    if len(shape) != dims:
+        raise ValueError(f"{name} must be a ({'B, T, C' if dims == 3 else 'B, C'}) tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return shape, dtype, device, _dtype_code_of(dtype)
 
 
-class _on:
-    """Make a tensor's device the current one for a call."""
-    __slots__ = ("index", "back")
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        import torch
-        now = torch._C._cuda_getDevice()
-        self.back = None
-        if self.index != now:
-            self.back = now
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            import torch
-            torch.cuda.set_device(self.back)
+def _dtype_code_of(dtype) -> int:
+    if dtype is _torch.bfloat16:
+        return VRWKV_BF16
+    if dtype is _torch.float32:
+        return VRWKV_F32
+    raise TypeError(f"unsupported dtype {dtype}")
 
 
 def _heads(shape, heads: int, what: str) -> int:
@@ -560,32 +556,58 @@ def _heads(shape, heads: int, what: str) -> int:
     return shape[-1] // heads
 
 
-def _workspace(need: int, workspace, device):
-    """The caller's workspace, or a new one of `need` bytes (None for 0)."""
-    if workspace is None:
-        if not need:
-            return None
-        import torch
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _require(workspace, "workspace")
-    if workspace.device != device:
-        raise ValueError(f"workspace must be on {device}")
-    return workspace
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
-def _ws_args(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _empty_rows(t, shape, dtype, device):
+    return _torch.empty_like(t) if t.is_contiguous() else _torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(key, size, workspace, device):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one of
+    the size remembered under key (size(): the library's answer)."""
+    if workspace is not None:
+        _require(workspace, "workspace")
+        if workspace.device != device:
+            raise ValueError(f"workspace must be on {device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    key = (device.index, *key)
+    need = _ws_need.get(key)
+    if need is None:
+        need = _ws_need[key] = int(size())
+    if not need:
+        return None, 0, None
+    t = _torch.empty(need, dtype=_torch.uint8, device=device)
+    return t.data_ptr(), need, t
+
+
+def _on_device(device, call):
+    """call() with `device` as the current one."""
+    now = _torch._C._cuda_getDevice()
+    if device.index == now:
+        return call()
+    _torch.cuda.set_device(device)
+    try:
+        return call()
+    finally:
+        _torch.cuda.set_device(now)
+
+
+def _workspace_tensor(size, device):
+    device = _torch.empty(0, device=device).device
+    n = int(_on_device(device, size))
+    return _torch.empty(max(n, 256), dtype=_torch.uint8, device=device)
 
 
 def decay_attn_workspace(B: int, T: int, heads: int, head_size: int, dtype, backward: bool = False, device="cuda"):
     """A uint8 CUDA tensor usable as the workspace of decay_attn_fwd (or, with
     backward, decay_attn_bwd) on problems of these sizes, one call at a time."""
-    import torch
-    device = torch.empty(0, device=device).device
-    code = VRWKV_F32 if dtype == torch.float32 else VRWKV_BF16
-    with _on(device):
-        n = int(load_library().vrwkv_decay_attn_workspace_bytes(B, T, int(heads), int(head_size), code, int(backward)))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    if _torch is None:
+        _load_torch()
+    code = _dtype_code_of(dtype)
+    return _workspace_tensor(
+        lambda: load_library().vrwkv_decay_attn_workspace_bytes(B, T, heads, head_size, code, int(backward)), device)
 
 
 def decay_attn_fwd(q, k, v, w, heads: int, scale: float = 1.0, state=None, lengths=None, want_state: bool = True,
@@ -599,34 +621,37 @@ def decay_attn_fwd(q, k, v, w, heads: int, scale: float = 1.0, state=None, lengt
     (B,), sequence b's valid tokens; rows past them are not used and give zeros.
     Returns out (B, T, C) and the state after the last token (state_out if
     given; it may be state itself; None if not wanted)."""
-    import torch
-    if q.dim() != 3:
-        raise ValueError("q must be a (B, T, C) tensor")
-    shape_q, dtype, dev = q.shape, q.dtype, q.device
-    B, T, C = shape_q
-    D, code = _heads(shape_q, heads, "q"), _dtype_code(q)
-    ldq, ldk, ldv = (_require_rows("q", q, shape_q, dtype, dev), _require_rows("k", k, shape_q, dtype, dev),
-                     _require_rows("v", v, shape_q, dtype, dev))
+    if _torch is None:
+        _load_torch()
+    shape, dtype, dev, code = _tokens_of("q", q, 3)
+    B, T, C = shape
+    D = _heads(shape, heads, "q")
+    ldq = C if q.is_contiguous() else _row_stride("q", q, shape)
+    ldk, ldv = _require_rows("k", k, shape, dtype, dev), _require_rows("v", v, shape, dtype, dev)
     _require_f32("w", w, (heads,), dev)
-    shape = (B, heads, D, D)
-    for n, t in (("state", state), ("state_out", state_out)):
-        if t is not None:
-            _require_f32(n, t, shape, dev)
+    states = (B, heads, D, D)
+    if state is not None:
+        _require_f32("state", state, states, dev)
+    if state_out is not None:
+        _require_f32("state_out", state_out, states, dev)
     if lengths is not None:
         _require_ints("lengths", lengths, B, dev)
-    if out is None:
-        out = torch.empty(shape_q, dtype=dtype, device=dev)
+    if out is not None:
+        _require_like("out", out, shape, dtype, dev, "q")
     else:
-        _require_like("out", out, shape_q, dtype, dev, "q")
+        out = _empty_rows(q, shape, dtype, dev)
     if state_out is None and want_state:
-        state_out = torch.empty(shape, dtype=torch.float32, device=dev)
+        state_out = _torch.empty(states, dtype=_torch.float32, device=dev)
     lib = load_library()
-    with _on(dev):
-        need = 0 if workspace is not None else int(lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 0))
-        ws = _workspace(need, workspace, dev)
-        _check(lib.vrwkv_decay_attn_fwd(
+
+    def call():
+        ws, n, keep = _workspace((B, T, heads, D, code, 0),
+                                 lambda: lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 0), workspace, dev)
+        return lib.vrwkv_decay_attn_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, w.data_ptr(), _ptr(state), _ptr(lengths), scale,
-            out.data_ptr(), _ptr(state_out), B, T, heads, D, code, *_ws_args(ws), _stream_of(dev)))
+            out.data_ptr(), _ptr(state_out), B, T, heads, D, code, ws, n, _torch._C._cuda_getCurrentRawStream(dev.index))
+
+    _check(_on_device(dev, call))
     return out, state_out
 
 
@@ -637,35 +662,42 @@ def decay_attn_bwd(q, k, v, w, heads: int, gy, scale: float = 1.0, state=None, g
     is given, its gradient (else None).  w is a constant: no gradient.
     out: optional (gq, gk, gv, gstate_in or None) to write instead of
     allocating them."""
-    import torch
-    if q.dim() != 3:
-        raise ValueError("q must be a (B, T, C) tensor")
-    shape_q, dtype, dev = q.shape, q.dtype, q.device
-    B, T, C = shape_q
-    D, code = _heads(shape_q, heads, "q"), _dtype_code(q)
-    ld = [_require_rows(n, t, shape_q, dtype, dev) for n, t in (("q", q), ("k", k), ("v", v), ("gy", gy))]
+    if _torch is None:
+        _load_torch()
+    shape, dtype, dev, code = _tokens_of("q", q, 3)
+    B, T, C = shape
+    D = _heads(shape, heads, "q")
+    ldq = C if q.is_contiguous() else _row_stride("q", q, shape)
+    ldk, ldv = _require_rows("k", k, shape, dtype, dev), _require_rows("v", v, shape, dtype, dev)
+    ldg = _require_rows("gy", gy, shape, dtype, dev)
     _require_f32("w", w, (heads,), dev)
-    shape = (B, heads, D, D)
+    states = (B, heads, D, D)
+    if state is not None:
+        _require_f32("state", state, states, dev)
+    if gstate is not None:
+        _require_f32("gstate", gstate, states, dev)
+    if lengths is not None:
+        _require_ints("lengths", lengths, B, dev)
     if out is None:
-        gq, gk, gv = (torch.empty((B, T, C), dtype=q.dtype, device=dev) for _ in range(3))
-        gs = None if state is None else torch.empty(shape, dtype=torch.float32, device=dev)
+        gq, gk, gv = (_torch.empty(shape, dtype=dtype, device=dev) for _ in range(3))
+        gs = None if state is None else _torch.empty(states, dtype=_torch.float32, device=dev)
     else:
         gq, gk, gv, gs = out
         for n, t in (("gq", gq), ("gk", gk), ("gv", gv)):
-            _require_like(n, t, shape_q, dtype, dev, "q")
-    for n, t in (("state", state), ("gstate", gstate), ("gstate_in", gs)):
-        if t is not None:
-            _require_f32(n, t, shape, dev)
-    if lengths is not None:
-        _require_ints("lengths", lengths, B, dev)
+            _require_like(n, t, shape, dtype, dev, "q")
+        if gs is not None:
+            _require_f32("gstate_in", gs, states, dev)
     lib = load_library()
-    with _on(dev):
-        need = 0 if workspace is not None else int(lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 1))
-        ws = _workspace(need, workspace, dev)
-        _check(lib.vrwkv_decay_attn_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), gy.data_ptr(), *ld, w.data_ptr(), _ptr(state), _ptr(gstate),
-            _ptr(lengths), scale, gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gs), B, T, heads, D, code,
-            *_ws_args(ws), _stream_of(dev)))
+
+    def call():
+        ws, n, keep = _workspace((B, T, heads, D, code, 1),
+                                 lambda: lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 1), workspace, dev)
+        return lib.vrwkv_decay_attn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), gy.data_ptr(), ldq, ldk, ldv, ldg, w.data_ptr(), _ptr(state),
+            _ptr(gstate), _ptr(lengths), scale, gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gs), B, T, heads, D,
+            code, ws, n, _torch._C._cuda_getCurrentRawStream(dev.index))
+
+    _check(_on_device(dev, call))
     return gq, gk, gv, gs
 
 
@@ -675,100 +707,107 @@ def decay_attn_step(q, k, v, w, heads: int, state, slots=None, scale: float = 1.
     int32 (B,), sequence b's place in it (default b).  A negative slot marks an
     idle row, whose output is zeros; a slot >= N or named by an earlier row too
     is treated so and reported by device_status().  Returns out (B, C)."""
-    import torch
-    if q.dim() != 2:
-        raise ValueError("q must be a (B, C) tensor")
-    shape_q, dtype, dev = q.shape, q.dtype, q.device
-    B, C = shape_q
-    D, code = _heads(shape_q, heads, "q"), _dtype_code(q)
-    ldq, ldk, ldv = (_require_rows("q", q, shape_q, dtype, dev), _require_rows("k", k, shape_q, dtype, dev),
-                     _require_rows("v", v, shape_q, dtype, dev))
+    if _torch is None:
+        _load_torch()
+    shape, dtype, dev, code = _tokens_of("q", q, 2)
+    B, C = shape
+    D = _heads(shape, heads, "q")
+    ldq = C if q.is_contiguous() else _row_stride("q", q, shape)
+    ldk, ldv = _require_rows("k", k, shape, dtype, dev), _require_rows("v", v, shape, dtype, dev)
     _require_f32("w", w, (heads,), dev)
-    if state.dim() != 4:
+    pool = state.shape
+    if len(pool) != 4:
         raise ValueError("state must be a (N, heads, D, D) tensor")
-    N = state.shape[0]
+    N = pool[0]
     _require_f32("state", state, (N, heads, D, D), dev)
     if slots is not None:
         _require_ints("slots", slots, B, dev)
     if out is None:
-        out = torch.empty(shape_q, dtype=dtype, device=dev)
+        out = _empty_rows(q, shape, dtype, dev)
     else:
-        _require_like("out", out, shape_q, dtype, dev, "q")
-    with _on(dev):
-        _check(load_library().vrwkv_decay_attn_step(
+        _require_like("out", out, shape, dtype, dev, "q")
+    lib = load_library()
+
+    def call():
+        return lib.vrwkv_decay_attn_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, w.data_ptr(), state.data_ptr(), _ptr(slots), scale,
-            out.data_ptr(), B, N, heads, D, code, _stream_of(dev)))
+            out.data_ptr(), B, N, heads, D, code, _torch._C._cuda_getCurrentRawStream(dev.index))
+
+    _check(_on_device(dev, call))
     return out
 
 
 def _norm_rows(x):
-    _require(x, "x")
-    if x.dim() < 1 or x.numel() == 0:
+    shape = x.shape
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA tensor")
+    n = x.numel()
+    if len(shape) < 1 or n == 0:
         raise ValueError("x must be a (..., C) tensor with rows")
-    return x.numel() // x.shape[-1], x.shape[-1]
+    return shape, n // shape[-1], shape[-1], x.dtype, x.device, _dtype_code_of(x.dtype)
 
 
 def layer_norm_fwd(x, gamma, beta, eps: float = 1e-5, stats: bool = True, out=None):
     """LayerNorm over the last dimension of a contiguous (..., C) tensor
     (vrwkv_layer_norm_fwd), gamma and beta float32 (C,).  Returns y and the rows'
     mean and rstd (float32, x's shape without C; None without stats)."""
-    import torch
-    rows, C = _norm_rows(x)
-    dev, shape = x.device, x.shape
+    if _torch is None:
+        _load_torch()
+    shape, rows, C, dtype, dev, code = _norm_rows(x)
     _require_f32("gamma", gamma, (C,), dev)
     _require_f32("beta", beta, (C,), dev)
     if out is None:
-        out = torch.empty_like(x)
+        out = _torch.empty_like(x)
     else:
-        _require_like("out", out, shape, x.dtype, dev, "x")
+        _require_like("out", out, shape, dtype, dev, "x")
     mean = rstd = None
     if stats:
-        mean, rstd = (torch.empty(shape[:-1], dtype=torch.float32, device=dev) for _ in range(2))
-    with _on(dev):
-        _check(load_library().vrwkv_layer_norm_fwd(
-            x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), eps, out.data_ptr(), _ptr(mean), _ptr(rstd), rows,
-            C, _dtype_code(x), _stream_of(dev)))
+        mean = _torch.empty(shape[:-1], dtype=_torch.float32, device=dev)
+        rstd = _torch.empty_like(mean)
+    lib = load_library()
+    _check(_on_device(dev, lambda: lib.vrwkv_layer_norm_fwd(
+        x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), eps, out.data_ptr(), _ptr(mean), _ptr(rstd), rows, C, code,
+        _torch._C._cuda_getCurrentRawStream(dev.index))))
     return out, mean, rstd
 
 
 def layer_norm_bwd_workspace(rows: int, C: int, dtype, device="cuda"):
     """A uint8 CUDA tensor usable as layer_norm_bwd's workspace, one call at a
     time."""
-    import torch
-    device = torch.empty(0, device=device).device
-    code = VRWKV_F32 if dtype == torch.float32 else VRWKV_BF16
-    with _on(device):
-        n = int(load_library().vrwkv_layer_norm_bwd_workspace_bytes(rows, C, code))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    if _torch is None:
+        _load_torch()
+    code = _dtype_code_of(dtype)
+    return _workspace_tensor(lambda: load_library().vrwkv_layer_norm_bwd_workspace_bytes(rows, C, code), device)
 
 
 def layer_norm_bwd(x, gamma, mean, rstd, gy, weight_grads: bool = True, out=None, workspace=None):
     """Gradients of layer_norm_fwd (vrwkv_layer_norm_bwd) from the mean and rstd
     it returned: gx like x, ggamma and gbeta float32 (C,) (None without
     weight_grads).  out: optional gx to write instead of allocating it."""
-    import torch
-    rows, C = _norm_rows(x)
-    dev, shape = x.device, x.shape
+    if _torch is None:
+        _load_torch()
+    shape, rows, C, dtype, dev, code = _norm_rows(x)
     _require_f32("gamma", gamma, (C,), dev)
     _require_f32("mean", mean, shape[:-1], dev)
     _require_f32("rstd", rstd, shape[:-1], dev)
-    _require_like("gy", gy, shape, x.dtype, dev, "x")
+    _require_like("gy", gy, shape, dtype, dev, "x")
     if out is None:
-        out = torch.empty_like(x)
+        out = _torch.empty_like(x)
     else:
-        _require_like("out", out, shape, x.dtype, dev, "x")
-    code = _dtype_code(x)
-    ggamma = torch.empty(C, dtype=torch.float32, device=dev) if weight_grads else None
-    gbeta = torch.empty(C, dtype=torch.float32, device=dev) if weight_grads else None
+        _require_like("out", out, shape, dtype, dev, "x")
+    ggamma = gbeta = None
+    if weight_grads:
+        ggamma, gbeta = _torch.empty_like(gamma), _torch.empty_like(gamma)
     lib = load_library()
-    with _on(dev):
-        need = 0
-        if weight_grads and workspace is None:
-            need = int(lib.vrwkv_layer_norm_bwd_workspace_bytes(rows, C, code))
-        ws = _workspace(need, workspace, dev)
-        _check(lib.vrwkv_layer_norm_bwd(
+
+    def call():
+        ws, n, keep = (None, 0, None) if not weight_grads else _workspace(
+            (rows, C, code), lambda: lib.vrwkv_layer_norm_bwd_workspace_bytes(rows, C, code), workspace, dev)
+        return lib.vrwkv_layer_norm_bwd(
             x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), gy.data_ptr(), out.data_ptr(),
-            _ptr(ggamma), _ptr(gbeta), rows, C, code, *_ws_args(ws), _stream_of(dev)))
+            _ptr(ggamma), _ptr(gbeta), rows, C, code, ws, n, _torch._C._cuda_getCurrentRawStream(dev.index))
+
+    _check(_on_device(dev, call))
     return out, ggamma, gbeta
 
 

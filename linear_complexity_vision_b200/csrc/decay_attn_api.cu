@@ -85,11 +85,12 @@ Cut plan(int B, int T, int H, int D, int nprob, bool tc) {
     return cut_into(T, (int)std::max<long long>(1, std::min<long long>(slots / heads, units / 2)));
 }
 
-// The tensor-core kernel takes bfloat16 heads of 64 or 128 channels;
+// The tensor-core kernels take bfloat16 heads of 64 or 128 channels;
 // VRWKV_DECAY_TC=0 keeps them on the FP32 pipes (diagnostics and tests).
-bool tc_sizes(int D, vrwkv_dtype dtype) {
+bool tc_sizes(int D, vrwkv_dtype dtype) { return dtype == VRWKV_BF16 && (D == 64 || D == 128); }
+bool tc_disabled() {
     const char* e = getenv("VRWKV_DECAY_TC");
-    return dtype == VRWKV_BF16 && (D == 64 || D == 128) && !(e && e[0] == '0' && e[1] == 0);
+    return e && e[0] == '0' && e[1] == 0;
 }
 
 size_t state_floats(int B, int H, int D, int nseg) { return (size_t)B * H * nseg * D * D; }
@@ -223,7 +224,7 @@ Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long*
     Launcher l = {};
     l.dtype = dtype;
     l.exact = state_leaves;
-    l.tc = tc_sizes(D, dtype);
+    l.tc = tc_sizes(D, dtype) && !tc_disabled();
     l.t.wide_out = 1;
     for (int i = 0; i < no; ++i) {
         l.tc = l.tc && aligned(outs[i], 16) && (D != 64 || encode_tokens(&l.t.omap[i], outs[i], H * D, B, T, H * D));

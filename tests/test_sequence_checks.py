@@ -165,6 +165,9 @@ def test_workspace_sizes(lib):
 # ---- the binding ----
 
 
+vk._load_torch()
+
+
 class Rows(FakeCuda):
     """A stand-in with strides."""
 
@@ -259,7 +262,7 @@ def test_layer_norm_binding_refuses():
     x = tok()
     with pytest.raises(ValueError, match="gamma must be"):
         vk.layer_norm_fwd(x, f32(C + 1), f32(C))
-    with pytest.raises(ValueError, match="contiguous"):
+    with pytest.raises(ValueError, match="x must be a contiguous CUDA"):
         vk.layer_norm_fwd(FakeCuda((B, T, C), contiguous=False), f32(C), f32(C))
     with pytest.raises(ValueError, match="out must match"):
         vk.layer_norm_fwd(x, f32(C), f32(C), out=FakeCuda((B, C)))
