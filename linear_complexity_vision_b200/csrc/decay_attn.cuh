@@ -104,40 +104,48 @@ __device__ __forceinline__ float at4(const float4& v, int i) { return i == 0 ? v
 
 // The operator for any D <= DP (zero-padded) and either storage type, in
 // chunks of 32 tokens: inside a chunk the (32 x 32) products q.k weighted by
-// the decays, across chunks the state.  Thread (ty, tx) owns output columns
-// 4 tx + 64 c of rows ty + TY r, and the state's rows 4 ty + 64 r (DP 128, 64)
-// at the same columns, in registers; a copy of the state in shared memory
-// feeds the products with q.
+// the decays, across chunks the state.  A CTA takes 32 of the v channels (the
+// products with them and their columns of the state are independent of the
+// others; the products q.k are formed again in each of a head's DP / 32 CTAs,
+// at DP = 64 a sixth of the work, for twice the CTAs).  Thread (ty, tx) owns
+// output columns 4 tx .. +3 of rows ty and ty + 16, and the state's rows of
+// its ty at the same columns, in registers; a copy of the state in shared
+// memory feeds the products with q.  The next chunk's tiles are in registers
+// while one is worked on.  Bound by FP32 issue and shared-memory loads.
+constexpr int kFpThreads = 128;
+constexpr int kFpCols = 32;
+
 template <int DP>
 struct Cfg {
-    static constexpr int kThreads = 256;
     static constexpr int C = 32;                            // tokens of a chunk
-    static constexpr int TX = DP / 4 < 16 ? DP / 4 : 16;    // threads along the columns
-    static constexpr int TY = kThreads / TX;
-    static constexpr int R = C / TY;                        // output rows of a thread
-    static constexpr int NC = DP / 4 / TX;                  // its column groups of 4
     static constexpr int LD = DP + 4;                       // padded row: rows 1 apart are 4 banks apart
-    static constexpr int SR = DP * DP / (kThreads * 4 * NC);  // state rows of a thread
+    static constexpr int LV = kFpCols + 4;
+    static constexpr int SR = DP / 16;                      // state rows of a thread
     static constexpr int SG = SR < 4 ? SR : 4;              // of which SG are adjacent
-    static constexpr int kPowers = C + 1;
-    static constexpr int kSmemFloats = 3 * C * LD + DP * LD + C * (C + 4) + kPowers;
+    static constexpr int NL = (2 * C * (DP / 4) + C * (kFpCols / 4)) / kFpThreads;  // float4s a thread loads
+    static constexpr int kSmemFloats = 2 * C * LD + C * LV + DP * LV + C * LV + C + 4;
+    static constexpr int kResident = DP == 128 ? 3 : DP == 64 ? 5 : 6;  // CTAs of an SM
 };
 
 template <typename IO, int DP>
-__global__ void __launch_bounds__(256) decay_attn_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kFpThreads, Cfg<DP>::kResident)
+    decay_attn_kernel(const __grid_constant__ Params p) {
     using F = Cfg<DP>;
-    constexpr int C = F::C, LD = F::LD, TX = F::TX, TY = F::TY, R = F::R, NC = F::NC, SR = F::SR, SG = F::SG;
+    constexpr int C = F::C, LD = F::LD, LV = F::LV, SR = F::SR, SG = F::SG, NL = F::NL, NS = DP / kFpCols;
     extern __shared__ __align__(16) float sm[];
-    float* sq = sm;
+    float* sq = sm;                         // [C][LD]
     float* sk = sq + C * LD;
-    float* sv = sk + C * LD;
-    float* sx = sv + C * LD;                // X [k channel][v channel]
-    float* sp = sx + DP * LD;               // weighted q.k [C][C + 4]
-    float* pw = sp + C * (C + 4);           // e^{-w n}, n = 0 .. C
-    const Problem& pr = p.pr[blockIdx.x % p.nprob];
-    const int sx_id = blockIdx.x / p.nprob, seg = sx_id % p.nseg, bh = sx_id / p.nseg, b = bh / p.H, h = bh % p.H;
-    const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
+    float* sv = sk + C * LD;                // [C][LV]
+    float* sx = sv + C * LV;                // X [k channel][LV]
+    float* sp = sx + DP * LV;               // weighted q.k [C][LV]
+    float* pw = sp + C * LV;                // e^{-w n}, n = 0 .. C
+    const int j0 = (blockIdx.x % NS) * kFpCols;                      // first v channel
+    const int sid = blockIdx.x / NS;
+    const Problem& pr = p.pr[sid % p.nprob];
+    const int hid = sid / p.nprob, seg = hid % p.nseg, bh = hid / p.nseg, b = bh / p.H, h = bh % p.H;
+    const int tid = threadIdx.x, tx = tid % 8, ty = tid / 8;
     const int D = p.D;
+    if (j0 >= D) return;
     const float w = __ldg(p.w + h);
     const int n_seq = seq_tokens(p.lengths, b, p.T);
     const int t0 = seg * p.seg_tokens;
@@ -148,173 +156,181 @@ __global__ void __launch_bounds__(256) decay_attn_kernel(const __grid_constant__
     const size_t dd = (size_t)D * D;
     const size_t xo = ((size_t)bh * p.nseg + seg) * dd;
     const bool want_out = pr.out != nullptr;
-
-    if (tid <= C) pw[tid] = decay_pow(w, tid);
-    // state registers: rows 4-aligned groups, columns 4 tx + 64 c
-    float4 X[SR][NC];
-#pragma unroll
-    for (int r = 0; r < SR; ++r) {
-        const int i = (r / SG) * (TY * SG) + ty * SG + r % SG;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int j = 4 * tx + 64 * c;
-            float e[4] = {0.f, 0.f, 0.f, 0.f};
-            if (pr.x_in && i < D) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (j + m < D)
-                        e[m] = __ldg(pr.x_in + xo + (pr.x_in_t ? (size_t)(j + m) * D + i : (size_t)i * D + j + m));
-            }
-            X[r][c] = make_float4(e[0], e[1], e[2], e[3]);
-        }
-    }
-
     const size_t row0 = (size_t)b * p.T + t0;
     const size_t col0 = (size_t)h * D;
     const int nchunk = (n + C - 1) / C;
+    const int j = j0 + 4 * tx;                                       // this thread's columns
+
+    // float4 x of a chunk's tiles: q, k (rows of DP) and v (rows of this CTA's columns), zero past the
+    // chunk's tokens and the head's channels
+    float4 next[NL];
+    auto place = [&](int x, int& which, int& r, int& c) {
+        constexpr int PQ = C * (DP / 4);
+        which = x < PQ ? 0 : x < 2 * PQ ? 1 : 2;
+        const int y = x - which * PQ, per = which == 2 ? kFpCols / 4 : DP / 4;
+        r = y / per;
+        c = 4 * (y % per);
+    };
+    auto fetch = [&](int ci) {
+        const int a = (rev ? nchunk - 1 - ci : ci) * C, m = min(C, n - a);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            int which, r, c;
+            place(i * kFpThreads + tid, which, r, c);
+            const int ch = c + (which == 2 ? j0 : 0);
+            next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < m && ch < D && (which != 0 || want_out)) {
+                const char* base = which == 0 ? pr.q : which == 1 ? pr.k : pr.v;
+                const long long ld = which == 0 ? pr.ldq : which == 1 ? pr.ldk : pr.ldv;
+                const char* src = base + ((row0 + a + r) * (size_t)ld + col0 + ch) * es;
+                if (p.vec) {
+                    next[i] = ld4<IO>(src);
+                } else {
+                    next[i].x = Io<IO>::ld1(src);
+                    if (ch + 1 < D) next[i].y = Io<IO>::ld1(src + es);
+                    if (ch + 2 < D) next[i].z = Io<IO>::ld1(src + 2 * es);
+                    if (ch + 3 < D) next[i].w = Io<IO>::ld1(src + 3 * es);
+                }
+            }
+        }
+    };
+    if (nchunk > 0) fetch(0);
+    if (tid <= C) pw[tid] = decay_pow(w, tid);
+    // rows of the state a thread owns: SG adjacent ones per 16 * SG
+    auto state_row = [&](int r) { return (r / SG) * (16 * SG) + ty * SG + r % SG; };
+    float4 X[SR];
+#pragma unroll
+    for (int r = 0; r < SR; ++r) {
+        const int i = state_row(r);
+        float e[4] = {0.f, 0.f, 0.f, 0.f};
+        if (pr.x_in && i < D) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                if (j + m < D) e[m] = __ldg(pr.x_in + xo + (pr.x_in_t ? (size_t)(j + m) * D + i : (size_t)i * D + j + m));
+        }
+        X[r] = make_float4(e[0], e[1], e[2], e[3]);
+    }
+
     for (int ci = 0; ci < nchunk; ++ci) {
         const int a = (rev ? nchunk - 1 - ci : ci) * C;              // first token of the chunk, in the segment
         const int m = min(C, n - a);                                 // its tokens
+        const bool with_x = ci > 0 || pr.x_in != nullptr, update = ci + 1 < nchunk || pr.x_out != nullptr;
         __syncthreads();                                             // the previous chunk's readers are done
-        // tiles, zero past the chunk's tokens and the head's channels
-        for (int x = tid; x < 3 * C * (DP / 4); x += F::kThreads) {
-            const int which = x / (C * (DP / 4)), y = x % (C * (DP / 4)), r = y / (DP / 4), c = 4 * (y % (DP / 4));
-            if (which == 0 && !want_out) continue;
-            const char* base = which == 0 ? pr.q : which == 1 ? pr.k : pr.v;
-            const long long ld = which == 0 ? pr.ldq : which == 1 ? pr.ldk : pr.ldv;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < m && c < D) {
-                const char* src = base + ((row0 + a + r) * (size_t)ld + col0 + c) * es;
-                if (p.vec) {
-                    f = ld4<IO>(src);
-                } else {
-                    f.x = Io<IO>::ld1(src);
-                    if (c + 1 < D) f.y = Io<IO>::ld1(src + es);
-                    if (c + 2 < D) f.z = Io<IO>::ld1(src + 2 * es);
-                    if (c + 3 < D) f.w = Io<IO>::ld1(src + 3 * es);
-                }
-            }
-            float* dst = (which == 0 ? sq : which == 1 ? sk : sv) + r * LD + c;
-            *reinterpret_cast<float4*>(dst) = f;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            int which, r, c;
+            place(i * kFpThreads + tid, which, r, c);
+            *reinterpret_cast<float4*>(which == 2 ? sv + r * LV + c : (which ? sk : sq) + r * LD + c) = next[i];
         }
-        if (want_out) {
+        if (want_out && with_x) {
 #pragma unroll
-            for (int r = 0; r < SR; ++r) {
-                const int i = (r / SG) * (TY * SG) + ty * SG + r % SG;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) *reinterpret_cast<float4*>(sx + i * LD + 4 * tx + 64 * c) = X[r][c];
-            }
+            for (int r = 0; r < SR; ++r) *reinterpret_cast<float4*>(sx + state_row(r) * LV + 4 * tx) = X[r];
         }
         __syncthreads();
+        if (ci + 1 < nchunk) fetch(ci + 1);
         if (want_out) {
-            // weighted products: rows py, py + 16, columns px, px + 16
-            const int py = tid / 16, px = tid % 16;
-            float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+            // weighted products: rows ty, ty + 16, columns tx + 8 z; the far quarter has no past
+            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 4
             for (int i = 0; i < DP; i += 4) {
-                float4 qa[2], kb[2];
+                float4 qa[2], kb[4];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    qa[y] = *reinterpret_cast<const float4*>(sq + (py + 16 * y) * LD + i);
-                    kb[y] = *reinterpret_cast<const float4*>(sk + (px + 16 * y) * LD + i);
-                }
+                for (int y = 0; y < 2; ++y) qa[y] = *reinterpret_cast<const float4*>(sq + (ty + 16 * y) * LD + i);
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int z = 0; z < 4; ++z) kb[z] = *reinterpret_cast<const float4*>(sk + (tx + 8 * z) * LD + i);
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
+                for (int z = 0; z < 4; ++z) {
+                    const int near = z < 2 ? 0 : 1;                  // (0, z) and (1, z), less one of the far quarters
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        if (y != near && (rev ? y > near : y < near)) continue;
                         acc[y][z] = fmaf(qa[y].x, kb[z].x, acc[y][z]);
                         acc[y][z] = fmaf(qa[y].y, kb[z].y, acc[y][z]);
                         acc[y][z] = fmaf(qa[y].z, kb[z].z, acc[y][z]);
                         acc[y][z] = fmaf(qa[y].w, kb[z].w, acc[y][z]);
                     }
+                }
             }
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const int d = rev ? px + 16 * z - py - 16 * y : py + 16 * y - px - 16 * z;
-                    sp[(py + 16 * y) * (C + 4) + px + 16 * z] = d < 0 ? 0.f : acc[y][z] * pw[d] * pr.scale_intra;
+                for (int z = 0; z < 4; ++z) {
+                    const int d = rev ? tx + 8 * z - ty - 16 * y : ty + 16 * y - tx - 8 * z;
+                    sp[(ty + 16 * y) * LV + tx + 8 * z] = d < 0 ? 0.f : acc[y][z] * pw[d] * pr.scale_intra;
                 }
             __syncthreads();
-            float4 o[R][NC];
+            float4 o[2];
+            o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (with_x) {
+#pragma unroll 4
+                for (int i = 0; i < DP; i += 4) {
+                    float4 qa[2];
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+                    for (int r = 0; r < 2; ++r) qa[r] = *reinterpret_cast<const float4*>(sq + (ty + 16 * r) * LD + i);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int i = 0; i < DP; i += 4) {
-                float4 qa[R];
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 xv = *reinterpret_cast<const float4*>(sx + (i + e) * LV + 4 * tx);
 #pragma unroll
-                for (int r = 0; r < R; ++r) qa[r] = *reinterpret_cast<const float4*>(sq + (ty + TY * r) * LD + i);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const float4 xv = *reinterpret_cast<const float4*>(sx + (i + e) * LD + 4 * tx + 64 * c);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) fma4(o[r][c], at4(qa[r], e), xv);
+                        for (int r = 0; r < 2; ++r) fma4(o[r], at4(qa[r], e), xv);
                     }
-            }
+                }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int row = ty + TY * r;
-                const int d = rev ? m - 1 - row : row;
-                const float f = row < m ? pw[d + e0] * pr.scale_inter : 0.f;
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    o[r][c] = make_float4(o[r][c].x * f, o[r][c].y * f, o[r][c].z * f, o[r][c].w * f);
+                for (int r = 0; r < 2; ++r) {
+                    const int row = ty + 16 * r, d = rev ? m - 1 - row : row;
+                    const float f = row < m ? pw[d + e0] * pr.scale_inter : 0.f;
+                    o[r] = make_float4(o[r].x * f, o[r].y * f, o[r].z * f, o[r].w * f);
+                }
             }
+            // in the half a row does not reach its products are zeros
 #pragma unroll 2
             for (int s = 0; s < C; s += 4) {
-                float4 pa[R];
+                const bool reach[2] = {!(!rev && s >= 16), !(rev && s < 16)};
+                float4 pa[2];
 #pragma unroll
-                for (int r = 0; r < R; ++r) pa[r] = *reinterpret_cast<const float4*>(sp + (ty + TY * r) * (C + 4) + s);
+                for (int r = 0; r < 2; ++r)
+                    if (reach[r]) pa[r] = *reinterpret_cast<const float4*>(sp + (ty + 16 * r) * LV + s);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 4; ++e) {
+                    const float4 vv = *reinterpret_cast<const float4*>(sv + (s + e) * LV + 4 * tx);
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const float4 vv = *reinterpret_cast<const float4*>(sv + (s + e) * LD + 4 * tx + 64 * c);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) fma4(o[r][c], at4(pa[r], e), vv);
-                    }
+                    for (int r = 0; r < 2; ++r)
+                        if (reach[r]) fma4(o[r], at4(pa[r], e), vv);
+                }
             }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int row = ty + TY * r;
-                if (row >= m) continue;
+            for (int r = 0; r < 2; ++r) {
+                const int row = ty + 16 * r;
+                if (row >= m || j >= D) continue;
+                char* dst = pr.out + ((row0 + a + row) * (size_t)p.H * D + col0 + j) * es;
+                if (p.vec) {
+                    st4<IO>(dst, o[r]);
+                } else {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int j = 4 * tx + 64 * c;
-                    if (j >= D) continue;
-                    char* dst = pr.out + ((row0 + a + row) * (size_t)p.H * D + col0 + j) * es;
-                    if (p.vec) {
-                        st4<IO>(dst, o[r][c]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (j + e < D) Io<IO>::st1(dst + e * es, at4(o[r][c], e));
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e < D) Io<IO>::st1(dst + e * es, at4(o[r], e));
                 }
             }
         }
-        if (ci + 1 == nchunk && !pr.x_out) break;                    // no one reads the last state
+        if (!update) break;                                          // no one reads the last state
         // X <- e^{-w m} X + sum_s f_s k_s^T v_s
         const float fx = pw[m];
 #pragma unroll
-        for (int r = 0; r < SR; ++r)
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-                X[r][c] = make_float4(X[r][c].x * fx, X[r][c].y * fx, X[r][c].z * fx, X[r][c].w * fx);
+        for (int r = 0; r < SR; ++r) X[r] = make_float4(X[r].x * fx, X[r].y * fx, X[r].z * fx, X[r].w * fx);
+#pragma unroll 4
         for (int s = 0; s < m; ++s) {
             const float f = pw[rev ? s + 1 : m - 1 - s] * pr.scale_upd;
-            float4 vv[NC];
+            float4 vv = *reinterpret_cast<const float4*>(sv + s * LV + 4 * tx);
+            vv = make_float4(vv.x * f, vv.y * f, vv.z * f, vv.w * f);
+            if constexpr (SG == 4) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) vv[c] = *reinterpret_cast<const float4*>(sv + s * LD + 4 * tx + 64 * c);
+                for (int g = 0; g < SR / 4; ++g) {
+                    const float4 kk = *reinterpret_cast<const float4*>(sk + s * LD + g * 64 + ty * 4);
 #pragma unroll
-            for (int r = 0; r < SR; ++r) {
-                const float kf = sk[s * LD + (r / SG) * (TY * SG) + ty * SG + r % SG] * f;
+                    for (int e = 0; e < 4; ++e) fma4(X[4 * g + e], at4(kk, e), vv);
+                }
+            } else {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) fma4(X[r][c], kf, vv[c]);
+                for (int r = 0; r < SR; ++r) fma4(X[r], sk[s * LD + state_row(r)], vv);
             }
         }
     }
@@ -322,20 +338,17 @@ __global__ void __launch_bounds__(256) decay_attn_kernel(const __grid_constant__
     if (pr.x_out) {
 #pragma unroll
         for (int r = 0; r < SR; ++r) {
-            const int i = (r / SG) * (TY * SG) + ty * SG + r % SG;
+            const int i = state_row(r);
             if (i >= D) continue;
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 4 * tx + 64 * c + e;
-                    if (j < D) pr.x_out[xo + (pr.x_out_t ? (size_t)j * D + i : (size_t)i * D + j)] = at4(X[r][c], e);
-                }
+            for (int e = 0; e < 4; ++e)
+                if (j + e < D) pr.x_out[xo + (pr.x_out_t ? (size_t)(j + e) * D + i : (size_t)i * D + j + e)] = at4(X[r], e);
         }
     }
     if (want_out) {  // rows past the sequence's end
-        for (int x = tid; x < (t_end - n) * D; x += F::kThreads)
-            Io<IO>::st1(pr.out + ((row0 + n + x / D) * (size_t)p.H * D + col0 + x % D) * es, 0.f);
+        const int cols = min(kFpCols, D - j0);
+        for (int x = tid; x < (t_end - n) * cols; x += kFpThreads)
+            Io<IO>::st1(pr.out + ((row0 + n + x / cols) * (size_t)p.H * D + col0 + j0 + x % cols) * es, 0.f);
     }
 }
 

@@ -114,14 +114,14 @@ vrwkv_status launch_dp(const decay::Params& p, long long ctas, cudaStream_t s) {
     constexpr int smem = decay::Cfg<DP>::kSmemFloats * 4;
     const cudaError_t e = ensure_smem(decay::decay_attn_kernel<IO, DP>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    decay::decay_attn_kernel<IO, DP><<<(unsigned)ctas, decay::Cfg<DP>::kThreads, smem, s>>>(p);
+    decay::decay_attn_kernel<IO, DP><<<(unsigned)(ctas * (DP / decay::kFpCols)), decay::kFpThreads, smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_kernel launch");
 }
 
 template <typename IO>
 vrwkv_status launch_io(const decay::Params& p, cudaStream_t s) {
     const long long ctas = (long long)p.B * p.H * p.nseg * p.nprob;
-    if (ctas > INT_MAX) return fail(VRWKV_ERR_UNSUPPORTED, "too many heads (B*H = %lld)", (long long)p.B * p.H);
+    if (ctas > INT_MAX / 4) return fail(VRWKV_ERR_UNSUPPORTED, "too many heads (B*H = %lld)", (long long)p.B * p.H);
     switch (padded_d(p.D)) {
     case 32: return launch_dp<IO, 32>(p, ctas, s);
     case 64: return launch_dp<IO, 64>(p, ctas, s);
