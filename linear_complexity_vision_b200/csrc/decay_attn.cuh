@@ -1,4 +1,4 @@
-// Multi-head decay attention on the FP32 pipes: causal linear attention whose
+// Multi-head decay attention for any head size and type: causal linear attention whose
 // (D, D) state of each head decays by e^{-w} per token,
 //
 //   out_t = scale_intra * sum_{s <= t} e^{-w (t-s)} (q_t . k_s) v_s
@@ -85,131 +85,158 @@ __device__ __forceinline__ float4 ld4(const char* p) {
     return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
                        __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
 }
-template <typename IO>
-__device__ __forceinline__ void st4(char* p, float4 v) {
-    if (sizeof(IO) == 4) {
-        *reinterpret_cast<float4*>(p) = v;
-    } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        *reinterpret_cast<uint2*>(p) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
-}
-
-__device__ __forceinline__ void fma4(float4& a, float s, const float4& b) {
-    const float2 lo = fma2(f2(s), f2(b.x, b.y), f2(a.x, a.y)), hi = fma2(f2(s), f2(b.z, b.w), f2(a.z, a.w));
-    a = make_float4(lo.x, lo.y, hi.x, hi.y);
-}
-__device__ __forceinline__ float at4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
+// ---------------------------------------------------------------------------
 // The operator for any D <= DP (zero-padded) and either storage type, in
-// chunks of 32 tokens: inside a chunk the (32 x 32) products q.k weighted by
-// the decays, across chunks the state.  A CTA takes 32 of the v channels (the
-// products with them and their columns of the state are independent of the
-// others; the products q.k are formed again in each of a head's DP / 32 CTAs,
-// at DP = 64 a sixth of the work, for twice the CTAs).  Thread (ty, tx) owns
-// output columns 4 tx .. +3 of rows ty and ty + 16, and the state's rows of
-// its ty at the same columns, in registers; a copy of the state in shared
-// memory feeds the products with q.  The next chunk's tiles are in registers
-// while one is worked on.  Bound by FP32 issue and shared-memory loads.
-constexpr int kFpThreads = 128;
-constexpr int kFpCols = 32;
-
+// chunks of 32 tokens: inside a chunk the products q.k weighted by the decays,
+// across chunks the state X.  The products run on the warp-level tensor cores
+// as tf32 (m16n8k8): a float32 operand is split into a tf32 value and the
+// remainder as another, hi hi + hi lo + lo hi (what is left out is 2^-22 of a
+// product); a bfloat16 operand is a tf32 value as it stands.  The tensor cores
+// truncate when they add, so a chain is two instructions' sums long (16
+// products) and joins the float32 sums on the FP32 pipes.
+// Why not the FP32 pipes: fed from shared memory with 8 products an operand
+// they measured a quarter of their rate (float32 B=8 T=1024 16 heads of 64:
+// 223 us), while a fragment of m16n8k8 serves 16 products and more.
+//
+// Warps: the token tiles of 16 rows (2), times 2 (DP = 128: 4) parts of the v
+// channels.  X^T is kept in registers, 16 v channels a warp (at DP = 32 with
+// half of the k channels), and copied to shared memory for q X.  The next
+// chunk's tiles are on their way in registers while one is worked on.  Sums over
+// tokens take them in the order 2t, 2t + 1 of a group of 8 that the
+// accumulator layout has, so P goes from accumulators to operands in place;
+// with rows of DP + 4 floats every fragment load is free of bank conflicts.
+// ---------------------------------------------------------------------------
 template <int DP>
 struct Cfg {
     static constexpr int C = 32;                            // tokens of a chunk
-    static constexpr int LD = DP + 4;                       // padded row: rows 1 apart are 4 banks apart
-    static constexpr int LV = kFpCols + 4;
-    static constexpr int SR = DP / 16;                      // state rows of a thread
-    static constexpr int SG = SR < 4 ? SR : 4;              // of which SG are adjacent
-    static constexpr int NL = (2 * C * (DP / 4) + C * (kFpCols / 4)) / kFpThreads;  // float4s a thread loads
-    static constexpr int kSmemFloats = 2 * C * LD + C * LV + DP * LV + C * LV + C + 4;
-    static constexpr int kResident = DP == 128 ? 3 : DP == 64 ? 5 : 6;  // CTAs of an SM
+    static constexpr int LD = DP + 4;
+    static constexpr int kWarps = DP == 128 ? 8 : 4;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int NT = DP / 8 / (kWarps / 2);        // 8-channel tiles of a warp's output rows
+    static constexpr int NL = 3 * C * (DP / 4) / kThreads;  // float4s a thread loads
+    static constexpr int UM = DP / 16;                      // 16-channel tiles of X^T's rows
+    static constexpr int UT = DP / 8 / (kWarps / UM);       // 8-channel tiles of a warp's part of X^T
+    static constexpr int kSmemFloats = 3 * C * LD + DP * LD + C + 4;
+    static constexpr int kResident = DP == 128 ? 1 : 3;     // CTAs of an SM, by registers
 };
 
+// A float32 operand as tf32 values: hi to nearest, lo the remainder (of which
+// the tensor core reads the upper bits, so half a step is added first).
+template <bool EXACT>
+__device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) {
+    if (EXACT) {
+        hi = __float_as_uint(x);
+        lo = 0u;
+    } else {
+        hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+        lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+    }
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An A operand of two steps (16 summed indices), and a product with a B operand
+// of two steps added to c.  AX, BX: the operand is exactly tf32.
+struct FragA {
+    uint32_t hi[2][4], lo[2][4];
+    template <bool AX>
+    __device__ __forceinline__ void set(int step, float a0, float a1, float a2, float a3) {
+        tf32_split<AX>(a0, hi[step][0], lo[step][0]);
+        tf32_split<AX>(a1, hi[step][1], lo[step][1]);
+        tf32_split<AX>(a2, hi[step][2], lo[step][2]);
+        tf32_split<AX>(a3, hi[step][3], lo[step][3]);
+    }
+};
+template <bool AX, bool BX>
+__device__ __forceinline__ void mma_pair(float (&c)[4], const FragA& a, float b00, float b01, float b10, float b11) {
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t h[4], l[4];
+    tf32_split<BX>(b00, h[0], l[0]);
+    tf32_split<BX>(b01, h[1], l[1]);
+    tf32_split<BX>(b10, h[2], l[2]);
+    tf32_split<BX>(b11, h[3], l[3]);
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+        if (!AX) mma_tf32(t, a.lo[step], h[2 * step], h[2 * step + 1]);
+        if (!BX) mma_tf32(t, a.hi[step], l[2 * step], l[2 * step + 1]);
+        mma_tf32(t, a.hi[step], h[2 * step], h[2 * step + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] += t[i];
+}
+
 template <typename IO, int DP>
-__global__ void __launch_bounds__(kFpThreads, Cfg<DP>::kResident)
+__global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
     decay_attn_kernel(const __grid_constant__ Params p) {
     using F = Cfg<DP>;
-    constexpr int C = F::C, LD = F::LD, LV = F::LV, SR = F::SR, SG = F::SG, NL = F::NL, NS = DP / kFpCols;
+    constexpr int C = F::C, LD = F::LD, NT = F::NT, UT = F::UT, UM = F::UM, kThreads = F::kThreads;
+    constexpr bool IX = sizeof(IO) == 2;     // inputs are exactly tf32
+    constexpr int es = sizeof(IO);
     extern __shared__ __align__(16) float sm[];
-    float* sq = sm;                         // [C][LD]
+    float* sq = sm;                          // [token][LD]
     float* sk = sq + C * LD;
-    float* sv = sk + C * LD;                // [C][LV]
-    float* sx = sv + C * LV;                // X [k channel][LV]
-    float* sp = sx + DP * LV;               // weighted q.k [C][LV]
-    float* pw = sp + C * LV;                // e^{-w n}, n = 0 .. C
-    const int j0 = (blockIdx.x % NS) * kFpCols;                      // first v channel
-    const int sid = blockIdx.x / NS;
-    const Problem& pr = p.pr[sid % p.nprob];
-    const int hid = sid / p.nprob, seg = hid % p.nseg, bh = hid / p.nseg, b = bh / p.H, h = bh % p.H;
-    const int tid = threadIdx.x, tx = tid % 8, ty = tid / 8;
+    float* sv = sk + C * LD;
+    float* sx = sv + C * LD;                 // X^T [v channel][LD]
+    float* pw = sx + DP * LD;                // e^{-w n}, n = 0 .. C
+    const Problem& pr = p.pr[blockIdx.x % p.nprob];
+    const int hid = blockIdx.x / p.nprob, seg = hid % p.nseg, bh = hid / p.nseg, b = bh / p.H, h = bh % p.H;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int D = p.D;
-    if (j0 >= D) return;
     const float w = __ldg(p.w + h);
     const int n_seq = seq_tokens(p.lengths, b, p.T);
     const int t0 = seg * p.seg_tokens;
     const int n = seg_count(n_seq, seg, p.seg_tokens);               // valid tokens of this segment
     const int t_end = min(t0 + p.seg_tokens, p.T) - t0;              // its rows of the tensors
     const int rev = pr.reverse, e0 = rev ? 0 : 1;
-    constexpr int es = sizeof(IO);
-    const size_t dd = (size_t)D * D;
-    const size_t xo = ((size_t)bh * p.nseg + seg) * dd;
+    const size_t xo = ((size_t)bh * p.nseg + seg) * (size_t)D * D;
     const bool want_out = pr.out != nullptr;
     const size_t row0 = (size_t)b * p.T + t0;
     const size_t col0 = (size_t)h * D;
     const int nchunk = (n + C - 1) / C;
-    const int j = j0 + 4 * tx;                                       // this thread's columns
 
-    // float4 x of a chunk's tiles: q, k (rows of DP) and v (rows of this CTA's columns), zero past the
-    // chunk's tokens and the head's channels
+    if (tid <= C) pw[tid] = decay_pow(w, tid);
+    // this warp's rows of a chunk and first v channel of its output; its v and first k channel of X^T
+    const int mt = warp % 2, c0 = (warp / 2) * NT * 8;
+    const int um = (warp % UM) * 16, u0 = (warp / UM) * UT * 8;
+    float X[UT][4];                          // rows um + g, um + g + 8, columns u0 + 8 i + 2 t, + 1
+#pragma unroll
+    for (int i = 0; i < UT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int dv = um + g + (e >> 1) * 8, dk = u0 + 8 * i + 2 * t + (e & 1);
+            X[i][e] = pr.x_in && dv < D && dk < D
+                          ? __ldg(pr.x_in + xo + (pr.x_in_t ? (size_t)dv * D + dk : (size_t)dk * D + dv)) : 0.f;
+        }
+
+    // a thread's part of a chunk's q, k, v tiles, zero past the chunk's tokens and the head's channels
+    constexpr int NL = F::NL, kPer = NL / 3;
     float4 next[NL];
-    auto place = [&](int x, int& which, int& r, int& c) {
-        constexpr int PQ = C * (DP / 4);
-        which = x < PQ ? 0 : x < 2 * PQ ? 1 : 2;
-        const int y = x - which * PQ, per = which == 2 ? kFpCols / 4 : DP / 4;
-        r = y / per;
-        c = 4 * (y % per);
-    };
     auto fetch = [&](int ci) {
         const int a = (rev ? nchunk - 1 - ci : ci) * C, m = min(C, n - a);
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            int which, r, c;
-            place(i * kFpThreads + tid, which, r, c);
-            const int ch = c + (which == 2 ? j0 : 0);
+            const int which = i / kPer, y = (i % kPer) * kThreads + tid, r = y / (DP / 4), c = 4 * (y % (DP / 4));
             next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < m && ch < D && (which != 0 || want_out)) {
+            if (r < m && c < D && (which != 0 || want_out)) {
                 const char* base = which == 0 ? pr.q : which == 1 ? pr.k : pr.v;
                 const long long ld = which == 0 ? pr.ldq : which == 1 ? pr.ldk : pr.ldv;
-                const char* src = base + ((row0 + a + r) * (size_t)ld + col0 + ch) * es;
+                const char* src = base + ((row0 + a + r) * (size_t)ld + col0 + c) * es;
                 if (p.vec) {
                     next[i] = ld4<IO>(src);
                 } else {
                     next[i].x = Io<IO>::ld1(src);
-                    if (ch + 1 < D) next[i].y = Io<IO>::ld1(src + es);
-                    if (ch + 2 < D) next[i].z = Io<IO>::ld1(src + 2 * es);
-                    if (ch + 3 < D) next[i].w = Io<IO>::ld1(src + 3 * es);
+                    if (c + 1 < D) next[i].y = Io<IO>::ld1(src + es);
+                    if (c + 2 < D) next[i].z = Io<IO>::ld1(src + 2 * es);
+                    if (c + 3 < D) next[i].w = Io<IO>::ld1(src + 3 * es);
                 }
             }
         }
     };
     if (nchunk > 0) fetch(0);
-    if (tid <= C) pw[tid] = decay_pow(w, tid);
-    // rows of the state a thread owns: SG adjacent ones per 16 * SG
-    auto state_row = [&](int r) { return (r / SG) * (16 * SG) + ty * SG + r % SG; };
-    float4 X[SR];
-#pragma unroll
-    for (int r = 0; r < SR; ++r) {
-        const int i = state_row(r);
-        float e[4] = {0.f, 0.f, 0.f, 0.f};
-        if (pr.x_in && i < D) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                if (j + m < D) e[m] = __ldg(pr.x_in + xo + (pr.x_in_t ? (size_t)(j + m) * D + i : (size_t)i * D + j + m));
-        }
-        X[r] = make_float4(e[0], e[1], e[2], e[3]);
-    }
 
     for (int ci = 0; ci < nchunk; ++ci) {
         const int a = (rev ? nchunk - 1 - ci : ci) * C;              // first token of the chunk, in the segment
@@ -218,137 +245,139 @@ __global__ void __launch_bounds__(kFpThreads, Cfg<DP>::kResident)
         __syncthreads();                                             // the previous chunk's readers are done
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            int which, r, c;
-            place(i * kFpThreads + tid, which, r, c);
-            *reinterpret_cast<float4*>(which == 2 ? sv + r * LV + c : (which ? sk : sq) + r * LD + c) = next[i];
+            const int which = i / kPer, y = (i % kPer) * kThreads + tid;
+            *reinterpret_cast<float4*>((which == 0 ? sq : which == 1 ? sk : sv) + y / (DP / 4) * LD + 4 * (y % (DP / 4))) =
+                next[i];
         }
         if (want_out && with_x) {
 #pragma unroll
-            for (int r = 0; r < SR; ++r) *reinterpret_cast<float4*>(sx + state_row(r) * LV + 4 * tx) = X[r];
+            for (int i = 0; i < UT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<float2*>(sx + (um + g + 8 * e) * LD + u0 + 8 * i + 2 * t) = f2(X[i][2 * e], X[i][2 * e + 1]);
         }
         __syncthreads();
         if (ci + 1 < nchunk) fetch(ci + 1);
-        if (want_out) {
-            // weighted products: rows ty, ty + 16, columns tx + 8 z; the far quarter has no past
-            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll 4
-            for (int i = 0; i < DP; i += 4) {
-                float4 qa[2], kb[4];
+        if (want_out && 16 * mt < m) {
+            // O = q X and A = q k^T share q's fragments.  Of A, the tiles in these rows' past.
+            float o[NT][4], A[4][4];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) qa[y] = *reinterpret_cast<const float4*>(sq + (ty + 16 * y) * LD + i);
+            for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 #pragma unroll
-                for (int z = 0; z < 4; ++z) kb[z] = *reinterpret_cast<const float4*>(sk + (tx + 8 * z) * LD + i);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int near = z < 2 ? 0 : 1;                  // (0, z) and (1, z), less one of the far quarters
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        if (y != near && (rev ? y > near : y < near)) continue;
-                        acc[y][z] = fmaf(qa[y].x, kb[z].x, acc[y][z]);
-                        acc[y][z] = fmaf(qa[y].y, kb[z].y, acc[y][z]);
-                        acc[y][z] = fmaf(qa[y].z, kb[z].z, acc[y][z]);
-                        acc[y][z] = fmaf(qa[y].w, kb[z].w, acc[y][z]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int d = rev ? tx + 8 * z - ty - 16 * y : ty + 16 * y - tx - 8 * z;
-                    sp[(ty + 16 * y) * LV + tx + 8 * z] = d < 0 ? 0.f : acc[y][z] * pw[d] * pr.scale_intra;
-                }
-            __syncthreads();
-            float4 o[2];
-            o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (with_x) {
-#pragma unroll 4
-                for (int i = 0; i < DP; i += 4) {
-                    float4 qa[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) qa[r] = *reinterpret_cast<const float4*>(sq + (ty + 16 * r) * LD + i);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 xv = *reinterpret_cast<const float4*>(sx + (i + e) * LV + 4 * tx);
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) fma4(o[r], at4(qa[r], e), xv);
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = ty + 16 * r, d = rev ? m - 1 - row : row;
-                    const float f = row < m ? pw[d + e0] * pr.scale_inter : 0.f;
-                    o[r] = make_float4(o[r].x * f, o[r].y * f, o[r].z * f, o[r].w * f);
-                }
-            }
-            // in the half a row does not reach its products are zeros
+            for (int i = 0; i < 4; ++i) A[i][0] = A[i][1] = A[i][2] = A[i][3] = 0.f;
+            auto reach = [&](int i) { return (rev ? i >= 2 * mt : i <= 2 * mt + 1) && 8 * i < m; };
+            const float* qr = sq + (16 * mt + g) * LD + t;
 #pragma unroll 2
-            for (int s = 0; s < C; s += 4) {
-                const bool reach[2] = {!(!rev && s >= 16), !(rev && s < 16)};
-                float4 pa[2];
+            for (int k = 0; k < DP; k += 16) {
+                FragA fq;
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    if (reach[r]) pa[r] = *reinterpret_cast<const float4*>(sp + (ty + 16 * r) * LV + s);
+                for (int s = 0; s < 2; ++s)
+                    fq.set<IX>(s, qr[k + 8 * s], qr[8 * LD + k + 8 * s], qr[k + 8 * s + 4], qr[8 * LD + k + 8 * s + 4]);
+                if (with_x) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const float* x = sx + (c0 + 8 * i + g) * LD + k + t;
+                        mma_pair<IX, false>(o[i], fq, x[0], x[4], x[8], x[12]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!reach(i)) continue;
+                    const float* kk = sk + (8 * i + g) * LD + k + t;
+                    mma_pair<IX, IX>(A[i], fq, kk[0], kk[4], kk[8], kk[12]);
+                }
+            }
+            if (with_x) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 16 * mt + g + 8 * e;
+                    f[e] = pw[max(rev ? m - 1 - row : row, 0) + e0] * pr.scale_inter;
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][e] *= f[e >> 1];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!reach(i)) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float4 vv = *reinterpret_cast<const float4*>(sv + (s + e) * LV + 4 * tx);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        if (reach[r]) fma4(o[r], at4(pa[r], e), vv);
+                    const int r = 16 * mt + g + 8 * (e >> 1), c = 8 * i + 2 * t + (e & 1), d = rev ? c - r : r - c;
+                    A[i][e] = d < 0 ? 0.f : A[i][e] * pw[d] * pr.scale_intra;
                 }
             }
+            // O += P v, two tiles of P (16 tokens) at a time
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = ty + 16 * r;
-                if (row >= m || j >= D) continue;
-                char* dst = pr.out + ((row0 + a + row) * (size_t)p.H * D + col0 + j) * es;
-                if (p.vec) {
-                    st4<IO>(dst, o[r]);
-                } else {
+            for (int i = 0; i < 4; i += 2) {
+                if (!reach(i) && !reach(i + 1)) continue;
+                FragA fp;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j + e < D) Io<IO>::st1(dst + e * es, at4(o[r], e));
+                for (int s = 0; s < 2; ++s) fp.set<false>(s, A[i + s][0], A[i + s][2], A[i + s][1], A[i + s][3]);
+                const float* vv = sv + (8 * i + 2 * t) * LD + c0 + g;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    mma_pair<false, IX>(o[j], fp, vv[8 * j], vv[LD + 8 * j], vv[8 * LD + 8 * j], vv[9 * LD + 8 * j]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 16 * mt + g + 8 * e;
+                if (row >= m) continue;
+                char* dst = pr.out + ((row0 + a + row) * (size_t)p.H * D + col0) * es;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int c = c0 + 8 * j + 2 * t;
+                    if (p.vec) {  // D % 4 == 0: pairs are whole
+                        if (c < D) Io<IO>::st_pair(dst + c * es, f2(o[j][2 * e], o[j][2 * e + 1]));
+                    } else {
+                        if (c < D) Io<IO>::st1(dst + c * es, o[j][2 * e]);
+                        if (c + 1 < D) Io<IO>::st1(dst + (c + 1) * es, o[j][2 * e + 1]);
+                    }
                 }
             }
         }
         if (!update) break;                                          // no one reads the last state
-        // X <- e^{-w m} X + sum_s f_s k_s^T v_s
+        // X^T <- e^{-w m} X^T + sum_s f_s v_s^T k_s, 16 tokens at a time
+        float U[UT][4];
+#pragma unroll
+        for (int i = 0; i < UT; ++i) U[i][0] = U[i][1] = U[i][2] = U[i][3] = 0.f;
+#pragma unroll
+        for (int s0 = 0; s0 < C; s0 += 16) {
+            if (s0 >= m) break;
+            FragA fv;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int r = s0 + 8 * s + 2 * t;                    // tokens r and r + 1
+                const float f0 = r < m ? pw[rev ? r + 1 : m - 1 - r] * pr.scale_upd : 0.f;
+                const float f1 = r + 1 < m ? pw[rev ? r + 2 : m - 2 - r] * pr.scale_upd : 0.f;
+                const float* vv = sv + r * LD + um + g;
+                fv.set<false>(s, vv[0] * f0, vv[8] * f0, vv[LD] * f1, vv[LD + 8] * f1);
+            }
+            const float* kk = sk + (s0 + 2 * t) * LD + u0 + g;
+#pragma unroll
+            for (int i = 0; i < UT; ++i)
+                mma_pair<false, IX>(U[i], fv, kk[8 * i], kk[LD + 8 * i], kk[8 * LD + 8 * i], kk[9 * LD + 8 * i]);
+        }
         const float fx = pw[m];
 #pragma unroll
-        for (int r = 0; r < SR; ++r) X[r] = make_float4(X[r].x * fx, X[r].y * fx, X[r].z * fx, X[r].w * fx);
-#pragma unroll 4
-        for (int s = 0; s < m; ++s) {
-            const float f = pw[rev ? s + 1 : m - 1 - s] * pr.scale_upd;
-            float4 vv = *reinterpret_cast<const float4*>(sv + s * LV + 4 * tx);
-            vv = make_float4(vv.x * f, vv.y * f, vv.z * f, vv.w * f);
-            if constexpr (SG == 4) {
+        for (int i = 0; i < UT; ++i)
 #pragma unroll
-                for (int g = 0; g < SR / 4; ++g) {
-                    const float4 kk = *reinterpret_cast<const float4*>(sk + s * LD + g * 64 + ty * 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) fma4(X[4 * g + e], at4(kk, e), vv);
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < SR; ++r) fma4(X[r], sk[s * LD + state_row(r)], vv);
-            }
-        }
+            for (int e = 0; e < 4; ++e) X[i][e] = fmaf(fx, X[i][e], U[i][e]);
     }
 
     if (pr.x_out) {
 #pragma unroll
-        for (int r = 0; r < SR; ++r) {
-            const int i = state_row(r);
-            if (i >= D) continue;
+        for (int i = 0; i < UT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < D) pr.x_out[xo + (pr.x_out_t ? (size_t)(j + e) * D + i : (size_t)i * D + j + e)] = at4(X[r], e);
-        }
+            for (int e = 0; e < 4; ++e) {
+                const int dv = um + g + (e >> 1) * 8, dk = u0 + 8 * i + 2 * t + (e & 1);
+                if (dv < D && dk < D) pr.x_out[xo + (pr.x_out_t ? (size_t)dv * D + dk : (size_t)dk * D + dv)] = X[i][e];
+            }
     }
     if (want_out) {  // rows past the sequence's end
-        const int cols = min(kFpCols, D - j0);
-        for (int x = tid; x < (t_end - n) * cols; x += kFpThreads)
-            Io<IO>::st1(pr.out + ((row0 + n + x / cols) * (size_t)p.H * D + col0 + j0 + x % cols) * es, 0.f);
+        for (int x = tid; x < (t_end - n) * D; x += kThreads)
+            Io<IO>::st1(pr.out + ((row0 + n + x / D) * (size_t)p.H * D + col0 + x % D) * es, 0.f);
     }
 }
 

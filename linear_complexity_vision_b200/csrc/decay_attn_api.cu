@@ -78,7 +78,7 @@ Cut cut_into(int T, int want) {
 // heads work.  As many as fill the SMs once with resident CTAs: 4 of 49 KB or
 // 1 of 123 KB on the FP32 pipes, 2 (D = 64) or 1 on the tensor cores.
 Cut plan(int B, int T, int H, int D, int nprob, bool tc) {
-    const int resident = tc ? 1 : (padded_d(D) == 128 ? 1 : 4);
+    const int resident = tc ? 1 : (padded_d(D) == 128 ? 1 : padded_d(D) == 64 ? 3 : 4);
     const long long heads = (long long)B * H * nprob;
     const long long slots = (long long)sm_count() * resident;
     const int units = (T + kSegUnit - 1) / kSegUnit;
@@ -114,7 +114,7 @@ vrwkv_status launch_dp(const decay::Params& p, long long ctas, cudaStream_t s) {
     constexpr int smem = decay::Cfg<DP>::kSmemFloats * 4;
     const cudaError_t e = ensure_smem(decay::decay_attn_kernel<IO, DP>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    decay::decay_attn_kernel<IO, DP><<<(unsigned)(ctas * (DP / decay::kFpCols)), decay::kFpThreads, smem, s>>>(p);
+    decay::decay_attn_kernel<IO, DP><<<(unsigned)ctas, decay::Cfg<DP>::kThreads, smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_kernel launch");
 }
 
