@@ -36,6 +36,7 @@ struct Problem {
     int x_in_t, x_out_t;    // stored transposed: [v channel][k channel]
     int reverse;
     float scale_intra, scale_inter, scale_upd;
+    int skip;               // without out: a segment whose own state is not needed, or -1
 };
 
 struct Params {
@@ -133,8 +134,7 @@ __device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) 
     }
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -151,22 +151,40 @@ struct FragA {
         tf32_split<AX>(a3, hi[step][3], lo[step][3]);
     }
 };
-template <bool AX, bool BX>
-__device__ __forceinline__ void mma_pair(float (&c)[4], const FragA& a, float b00, float b01, float b10, float b11) {
-    float t[4] = {0.f, 0.f, 0.f, 0.f};
-    uint32_t h[4], l[4];
-    tf32_split<BX>(b00, h[0], l[0]);
-    tf32_split<BX>(b01, h[1], l[1]);
-    tf32_split<BX>(b10, h[2], l[2]);
-    tf32_split<BX>(b11, h[3], l[3]);
+// N tiles at a time, instruction by instruction over the tiles: a tile's own
+// instructions wait for one another.  load(i, h): the tile's B values, two
+// steps of two.
+template <bool AX, bool BX, int N, typename Load>
+__device__ __forceinline__ void mma_tiles(float (*c)[4], const FragA& a, Load load) {
+    float t[N][4];
+    uint32_t h[N][4], l[N][4];
 #pragma unroll
-    for (int step = 0; step < 2; ++step) {
-        if (!AX) mma_tf32(t, a.lo[step], h[2 * step], h[2 * step + 1]);
-        if (!BX) mma_tf32(t, a.hi[step], l[2 * step], l[2 * step + 1]);
-        mma_tf32(t, a.hi[step], h[2 * step], h[2 * step + 1]);
+    for (int i = 0; i < N; ++i) {
+        float b[4];
+        load(i, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            tf32_split<BX>(b[e], h[i][e], l[i][e]);
+            t[i][e] = 0.f;
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] += t[i];
+    for (int step = 0; step < 2; ++step) {
+        if (!AX) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) mma_tf32(t[i], a.lo[step], h[i][2 * step], h[i][2 * step + 1]);
+        }
+        if (!BX) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) mma_tf32(t[i], a.hi[step], l[i][2 * step], l[i][2 * step + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) mma_tf32(t[i], a.hi[step], h[i][2 * step], h[i][2 * step + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[i][e] += t[i][e];
 }
 
 template <typename IO, int DP>
@@ -184,6 +202,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
     float* pw = sx + DP * LD;                // e^{-w n}, n = 0 .. C
     const Problem& pr = p.pr[blockIdx.x % p.nprob];
     const int hid = blockIdx.x / p.nprob, seg = hid % p.nseg, bh = hid / p.nseg, b = bh / p.H, h = bh % p.H;
+    if (!pr.out && seg == pr.skip) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int D = p.D;
     const float w = __ldg(p.w + h);
@@ -265,7 +284,6 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
             for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) A[i][0] = A[i][1] = A[i][2] = A[i][3] = 0.f;
-            auto reach = [&](int i) { return (rev ? i >= 2 * mt : i <= 2 * mt + 1) && 8 * i < m; };
             const float* qr = sq + (16 * mt + g) * LD + t;
 #pragma unroll 2
             for (int k = 0; k < DP; k += 16) {
@@ -273,18 +291,21 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     fq.set<IX>(s, qr[k + 8 * s], qr[8 * LD + k + 8 * s], qr[k + 8 * s + 4], qr[8 * LD + k + 8 * s + 4]);
-                if (with_x) {
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
+                if (with_x)
+                    mma_tiles<IX, false, NT>(o, fq, [&](int i, float (&v)[4]) {
                         const float* x = sx + (c0 + 8 * i + g) * LD + k + t;
-                        mma_pair<IX, false>(o[i], fq, x[0], x[4], x[8], x[12]);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!reach(i)) continue;
-                    const float* kk = sk + (8 * i + g) * LD + k + t;
-                    mma_pair<IX, IX>(A[i], fq, kk[0], kk[4], kk[8], kk[12]);
+                        v[0] = x[0], v[1] = x[4], v[2] = x[8], v[3] = x[12];
+                    });
+                auto keys = [&](int i, float (&v)[4]) {
+                    const float* x = sk + (8 * i + g) * LD + k + t;
+                    v[0] = x[0], v[1] = x[4], v[2] = x[8], v[3] = x[12];
+                };
+                // the upper rows reach the near half of the columns only
+                if (mt == (rev ? 1 : 0)) {
+                    if (rev) mma_tiles<IX, IX, 2>(A + 2, fq, [&](int i, float (&v)[4]) { keys(i + 2, v); });
+                    else mma_tiles<IX, IX, 2>(A, fq, keys);
+                } else {
+                    mma_tiles<IX, IX, 4>(A, fq, keys);
                 }
             }
             if (with_x) {
@@ -301,7 +322,6 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (!reach(i)) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = 16 * mt + g + 8 * (e >> 1), c = 8 * i + 2 * t + (e & 1), d = rev ? c - r : r - c;
@@ -311,14 +331,14 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
             // O += P v, two tiles of P (16 tokens) at a time
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-                if (!reach(i) && !reach(i + 1)) continue;
+                if (rev ? i < 2 * mt : i > 2 * mt) continue;         // all in these rows' future
                 FragA fp;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) fp.set<false>(s, A[i + s][0], A[i + s][2], A[i + s][1], A[i + s][3]);
-                const float* vv = sv + (8 * i + 2 * t) * LD + c0 + g;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    mma_pair<false, IX>(o[j], fp, vv[8 * j], vv[LD + 8 * j], vv[8 * LD + 8 * j], vv[9 * LD + 8 * j]);
+                mma_tiles<false, IX, NT>(o, fp, [&](int j, float (&v)[4]) {
+                    const float* x = sv + (8 * i + 2 * t) * LD + c0 + g + 8 * j;
+                    v[0] = x[0], v[1] = x[LD], v[2] = x[8 * LD], v[3] = x[9 * LD];
+                });
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -354,10 +374,13 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
                 const float* vv = sv + r * LD + um + g;
                 fv.set<false>(s, vv[0] * f0, vv[8] * f0, vv[LD] * f1, vv[LD + 8] * f1);
             }
-            const float* kk = sk + (s0 + 2 * t) * LD + u0 + g;
+            constexpr int UB = UT < 4 ? UT : 4;
 #pragma unroll
-            for (int i = 0; i < UT; ++i)
-                mma_pair<false, IX>(U[i], fv, kk[8 * i], kk[LD + 8 * i], kk[8 * LD + 8 * i], kk[9 * LD + 8 * i]);
+            for (int j = 0; j < UT; j += UB)
+                mma_tiles<false, IX, UB>(U + j, fv, [&](int i, float (&v)[4]) {
+                    const float* x = sk + (s0 + 2 * t) * LD + u0 + g + 8 * (i + j);
+                    v[0] = x[0], v[1] = x[LD], v[2] = x[8 * LD], v[3] = x[9 * LD];
+                });
         }
         const float fx = pw[m];
 #pragma unroll
@@ -384,9 +407,9 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
 // ---------------------------------------------------------------------------
 // Chain the segments' own states: on entry u[seg] is segment seg's X_out from
 // X_in = 0; on return it is the segment's X_in, and x_last, if given, the
-// state after the last segment.  One thread per state element, the segments
-// in order (last to first in reversed time); loads of the next segment do not
-// wait for the chain.
+// state after the last segment (whose own state is read for it alone).  The
+// segments in order, last to first in reversed time, a thread 4 (or 1) of a
+// head's elements; the loads of the next segments do not wait for the chain.
 // ---------------------------------------------------------------------------
 struct ChainProblem {
     float* u;             // [(b*H + h)*nseg + seg][D*D]
@@ -402,25 +425,53 @@ struct ChainParams {
     int seg_tokens, nseg;
 };
 
-__global__ void __launch_bounds__(256) decay_chain_kernel(const ChainParams p) {
-    const ChainProblem& pr = p.pr[blockIdx.z];
-    const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
-    const int i = blockIdx.y * 256 + threadIdx.x;
-    if (i >= p.dd) return;
-    const float w = __ldg(p.w + h);
-    const int n_seq = seq_tokens(p.lengths, b, p.T);
-    float x = pr.x0 ? __ldg(pr.x0 + (size_t)bh * p.dd + i) : 0.f;
+template <typename V>
+__device__ __forceinline__ void chain(const ChainParams& p, const ChainProblem& pr, int bh, int i, DecayBase w, int n_seq) {
+    constexpr int N = sizeof(V) / 4;
+    constexpr int kAhead = 8;
+    V x, own[kAhead];
+    float* xs = reinterpret_cast<float*>(&x);
+#pragma unroll
+    for (int e = 0; e < N; ++e) xs[e] = pr.x0 ? __ldg(pr.x0 + (size_t)bh * p.dd + i + e) : 0.f;
     float* u = pr.u + (size_t)bh * p.nseg * p.dd + i;
     const int step = pr.reverse ? -1 : 1;
     int seg = pr.reverse ? p.nseg - 1 : 0;
-    float next = u[(size_t)seg * p.dd];
-    for (int s = 0; s < p.nseg; ++s, seg += step) {
-        const float own = next;
-        if (s + 1 < p.nseg) next = u[(size_t)(seg + step) * p.dd];
-        u[(size_t)seg * p.dd] = x;
-        x = fmaf(decay_pow(w, seg_count(n_seq, seg, p.seg_tokens)), x, own);
+    const int reads = p.nseg - (pr.x_last ? 0 : 1);
+    // eight segments are read before any is written
+    for (int s0 = 0; s0 < reads; s0 += kAhead) {
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+            if (s0 + s < reads) own[s] = *reinterpret_cast<const V*>(u + (size_t)(seg + s * step) * p.dd);
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+            if (s0 + s >= reads) break;
+            *reinterpret_cast<V*>(u + (size_t)seg * p.dd) = x;
+            const float f = decay_pow(w, seg_count(n_seq, seg, p.seg_tokens));
+            const float* os = reinterpret_cast<const float*>(&own[s]);
+#pragma unroll
+            for (int e = 0; e < N; ++e) xs[e] = fmaf(f, xs[e], os[e]);
+            seg += step;
+        }
     }
-    if (pr.x_last) pr.x_last[(size_t)bh * p.dd + i] = x;
+    if (reads < p.nseg) {
+        *reinterpret_cast<V*>(u + (size_t)seg * p.dd) = x;
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) pr.x_last[(size_t)bh * p.dd + i + e] = xs[e];
+    }
+}
+
+__global__ void __launch_bounds__(256) decay_chain_kernel(const ChainParams p) {
+    const ChainProblem& pr = p.pr[blockIdx.z];
+    const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
+    const int x = blockIdx.y * 256 + threadIdx.x;
+    const DecayBase w = decay_base(__ldg(p.w + h));
+    const int n_seq = seq_tokens(p.lengths, b, p.T);
+    if (p.dd % 4 == 0) {
+        if (4 * x < p.dd) chain<float4>(p, pr, bh, 4 * x, w, n_seq);
+    } else if (x < p.dd) {
+        chain<float>(p, pr, bh, x, w, n_seq);
+    }
 }
 
 // ---------------------------------------------------------------------------

@@ -65,6 +65,19 @@ vrwkv_status check_workspace(const void* ws, size_t have, size_t need) {
 // ---- the cut into segments ----
 int padded_d(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 
+// One head's chunks run one after the other; segments let more CTAs than heads
+// work, for a pass over k and v that forms the states at the cuts and two more
+// launches.  The cut is the one of least estimated time, from what the kernels
+// measured alone on an SM, in us for a unit of 128 tokens (and how much of
+// that each further CTA on the same SM adds):
+//                         outputs          states only      CTAs of an SM
+//   tensor cores, D = 64  1.75             2.0 (+ 0.5)      1 (persistent), 2
+//   tensor cores, D = 128 4.2              3.0              1
+//   any size, DP = 32     9 (+ 0.6)        4 (+ 0.6)        3
+//             DP = 64     23 (+ 0.6)       9 (+ 0.6)        3
+//             DP = 128    45               18               1
+// Both sides measured: B = 1, T = 4096, 16 heads of 64, bfloat16: one segment
+// 56 us, eight 32 us; B = 8: one segment 62 us, two 130 us.
 struct Cut {
     int seg_tokens, nseg;
 };
@@ -74,15 +87,39 @@ Cut cut_into(int T, int want) {
     return Cut{per * kSegUnit, (units + per - 1) / per};
 }
 
-// One head's chunks run one after the other; segments let more CTAs than
-// heads work.  As many as fill the SMs once with resident CTAs: 4 of 49 KB or
-// 1 of 123 KB on the FP32 pipes, 2 (D = 64) or 1 on the tensor cores.
+struct PassCost {
+    double unit, share;
+    int resident;
+};
+double pass_us(long long ctas, int units, const PassCost& c) {
+    const long long per_sm = (ctas + sm_count() - 1) / sm_count(), rounds = per_sm / c.resident;
+    const int rest = (int)(per_sm % c.resident);
+    const double round = 1.0 + c.share * (c.resident - 1), last = rest ? 1.0 + c.share * (rest - 1) : 0.0;
+    return units * c.unit * (rounds * round + last) + 3.0;
+}
+
 Cut plan(int B, int T, int H, int D, int nprob, bool tc) {
-    const int resident = tc ? 1 : (padded_d(D) == 128 ? 1 : padded_d(D) == 64 ? 3 : 4);
-    const long long heads = (long long)B * H * nprob;
-    const long long slots = (long long)sm_count() * resident;
+    static const PassCost kOut[5] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}};
+    static const PassCost kState[5] = {{2.0, 0.5, 2}, {3.0, 0, 1}, {4, 0.6, 3}, {9, 0.6, 3}, {18, 0, 1}};
+    const int kind = tc ? (D == 64 ? 0 : 1) : (D <= 32 ? 2 : D <= 64 ? 3 : 4);
     const int units = (T + kSegUnit - 1) / kSegUnit;
-    return cut_into(T, (int)std::max<long long>(1, std::min<long long>(slots / heads, units / 2)));
+    const long long heads = (long long)B * H;
+    Cut best = cut_into(T, 1);
+    double least = pass_us(heads * nprob, units, kOut[kind]);
+    static const int kWays[] = {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
+    for (int want : kWays) {
+        if (want > units) break;
+        const Cut c = cut_into(T, want);
+        const int per = c.seg_tokens / kSegUnit, states = nprob == 1 ? 1 : 2;
+        const double us = pass_us(heads * nprob * c.nseg, per, kOut[kind]) +
+                          pass_us(heads * states * c.nseg, per, kState[kind]) + 5.0 +
+                          1e-6 * heads * states * c.nseg * D * D * 4;
+        if (us < 0.95 * least) {
+            least = us;
+            best = c;
+        }
+    }
+    return best;
 }
 
 // The tensor-core kernels take bfloat16 heads of 64 or 128 channels;
@@ -244,7 +281,8 @@ Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long*
 }
 
 vrwkv_status launch_chain(const decay::ChainParams& p, int bh, int nprob, cudaStream_t s) {
-    decay::decay_chain_kernel<<<dim3((unsigned)bh, (unsigned)((p.dd + 255) / 256), (unsigned)nprob), 256, 0, s>>>(p);
+    const int per = p.dd % 4 == 0 ? 1024 : 256;  // elements of a CTA
+    decay::decay_chain_kernel<<<dim3((unsigned)bh, (unsigned)((p.dd + per - 1) / per), (unsigned)nprob), 256, 0, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_chain_kernel launch");
 }
 
@@ -289,7 +327,8 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     const void* srcs[3] = {q, k, v};
     const void* dsts[1] = {out};
     const long long lds[3] = {ldq, ldk, ldv};
-    Launcher attn = make_launcher(dtype, srcs, lds, 3, dsts, 1, state_out != nullptr, B, T, H, D);
+    Launcher attn =
+        make_launcher(dtype, srcs, lds, 3, dsts, 1, state_out != nullptr, B, T, H, D);
     const Cut cut = plan(B, T, H, D, 1, attn.tc);
     decay::Params p = {};
     p.w = w;
@@ -315,6 +354,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     float* ws = static_cast<float*>(workspace);
     if (cut.nseg > 1) {
         pr.x_out = ws;
+        pr.skip = state_out ? -1 : cut.nseg - 1;
         st = attn.run(p, s);
         if (st != VRWKV_OK) return st;
         decay::ChainParams c = {};
@@ -330,6 +370,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
         if (st != VRWKV_OK) return st;
         pr.x_in = ws;
         pr.x_out = nullptr;
+        attn.exact = false;  // the chain handed the state out
     } else {
         pr.x_in = state;
         pr.x_out = state_out;
@@ -404,6 +445,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
         a.v = V;
         a.ldv = ldv;
         a.x_out = ws;
+        a.skip = cut.nseg - 1;
         a.scale_upd = 1.0f;
         decay::Problem& c = p.pr[1];
         c.k = Q;
@@ -411,6 +453,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
         c.v = G;
         c.ldv = ldg;
         c.x_out = wg;
+        c.skip = gstate_in ? -1 : 0;
         c.scale_upd = scale;
         c.reverse = 1;
         p.nprob = 2;
@@ -431,13 +474,14 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
         s_in = ws;
         g_in = wg;
         g_out = nullptr;
+        attn.exact = false;  // the chain handed the state's gradient out
     }
     p.nprob = 3;
     // gq: (g, v, k) forward in time on S^T
-    p.pr[0] = {G, V, K, static_cast<char*>(gq), ldg, ldv, ldk, s_in, nullptr, 1, 1, 0, scale, scale, 1.0f};
+    p.pr[0] = {G, V, K, static_cast<char*>(gq), ldg, ldv, ldk, s_in, nullptr, 1, 1, 0, scale, scale, 1.0f, -1};
     // gk: (v, g, q) in reversed time on (dL/dS)^T; gv: (k, q, g) on dL/dS
-    p.pr[1] = {V, G, Q, static_cast<char*>(gk), ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale};
-    p.pr[2] = {K, Q, G, static_cast<char*>(gv), ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale};
+    p.pr[1] = {V, G, Q, static_cast<char*>(gk), ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale, -1};
+    p.pr[2] = {K, Q, G, static_cast<char*>(gv), ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale, -1};
     st = attn.run(p, s);
     if (st == VRWKV_OK) set_last_kernel(!attn.tc ? "decay_attn_kernel" : D == 64 ? "decay_attn_tc64_kernel" : "decay_attn_tc_kernel");
     return st;

@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     const int prob = blockIdx.x % p.nprob;
     const Problem& pr = p.pr[prob];
     const int sid = blockIdx.x / p.nprob, seg = sid % p.nseg, bh = sid / p.nseg, b = bh / p.H, h = bh % p.H;
+    if (!OUT && seg == pr.skip) return;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, quad = warp & 3, wg = warp >> 2;
     const float w = __ldg(p.w + h);
     const int n_seq = seq_tokens(p.lengths, b, p.T);
