@@ -10,6 +10,7 @@
 #include "decay_attn.cuh"
 #include "decay_attn_tc.cuh"
 #include "decay_attn_tc64.cuh"
+#include "decay_attn_tcf.cuh"
 
 namespace {
 
@@ -76,6 +77,7 @@ int padded_d(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 //   any size, DP = 32     9 (+ 0.6)        4 (+ 0.6)        3
 //             DP = 64     23 (+ 0.6)       9 (+ 0.6)        3
 //             DP = 128    45               18               1
+//   float32, D = 64       4.6              3.0              1
 // Both sides measured: B = 1, T = 4096, 16 heads of 64, bfloat16: one segment
 // 56 us, eight 32 us; B = 8: one segment 62 us, two 130 us.
 struct Cut {
@@ -98,10 +100,10 @@ double pass_us(long long ctas, int units, const PassCost& c) {
     return units * c.unit * (rounds * round + last) + 3.0;
 }
 
-Cut plan(int B, int T, int H, int D, int nprob, bool tc) {
-    static const PassCost kOut[5] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}};
-    static const PassCost kState[5] = {{2.0, 0.5, 2}, {3.0, 0, 1}, {4, 0.6, 3}, {9, 0.6, 3}, {18, 0, 1}};
-    const int kind = tc ? (D == 64 ? 0 : 1) : (D <= 32 ? 2 : D <= 64 ? 3 : 4);
+Cut plan(int B, int T, int H, int D, vrwkv_dtype dtype, int nprob, bool tc) {
+    static const PassCost kOut[6] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}, {4.6, 0, 1}};
+    static const PassCost kState[6] = {{2.0, 0.5, 2}, {3.0, 0, 1}, {4, 0.6, 3}, {9, 0.6, 3}, {18, 0, 1}, {3.0, 0, 1}};
+    const int kind = tc ? (dtype == VRWKV_F32 ? 5 : D == 64 ? 0 : 1) : (D <= 32 ? 2 : D <= 64 ? 3 : 4);
     const int units = (T + kSegUnit - 1) / kSegUnit;
     const long long heads = (long long)B * H;
     Cut best = cut_into(T, 1);
@@ -122,9 +124,9 @@ Cut plan(int B, int T, int H, int D, int nprob, bool tc) {
     return best;
 }
 
-// The tensor-core kernels take bfloat16 heads of 64 or 128 channels;
-// VRWKV_DECAY_TC=0 keeps them on the FP32 pipes (diagnostics and tests).
-bool tc_sizes(int D, vrwkv_dtype dtype) { return dtype == VRWKV_BF16 && (D == 64 || D == 128); }
+// The tcgen05 kernels take heads of 64 channels and bfloat16 heads of 128;
+// VRWKV_DECAY_TC=0 keeps them on the kernel for any size (diagnostics and tests).
+bool tc_sizes(int D, vrwkv_dtype dtype) { return D == 64 || (dtype == VRWKV_BF16 && D == 128); }
 bool tc_disabled() {
     const char* e = getenv("VRWKV_DECAY_TC");
     return e && e[0] == '0' && e[1] == 0;
@@ -137,7 +139,7 @@ size_t state_floats(int B, int H, int D, int nseg) { return (size_t)B * H * nseg
 size_t ws_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
     size_t need = 0;
     for (int tc = 0; tc <= (tc_sizes(D, dtype) ? 1 : 0); ++tc) {
-        const Cut c = plan(B, T, H, D, backward ? 3 : 1, tc != 0);
+        const Cut c = plan(B, T, H, D, dtype, backward ? 3 : 1, tc != 0);
         if (c.nseg > 1)
             need = std::max(need, ((backward ? 2 : 1) * state_floats(B, H, D, c.nseg) * 4 + 255) / 256 * 256);
     }
@@ -178,7 +180,8 @@ bool encode_tokens(CUtensorMap* m, const void* x, long long ld, int B, int T, in
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool tma_ok(const void* x, long long ld) { return aligned(x, 16) && ld % 8 == 0 && ld < (1LL << 36); }
+// Rows that start on 16-byte boundaries (and a stride that TMA can hold).
+bool rows16(const void* x, long long ld, int es) { return aligned(x, 16) && ld * es % 16 == 0 && ld < (1LL << 36); }
 
 template <int D, bool OUT, int PIECES>
 vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
@@ -206,6 +209,16 @@ vrwkv_status launch_tc64(decay::TcParams& p, cudaStream_t s) {
     decay::decay_attn_tc64_kernel<PIECES, PP><<<ctas, decay::kT64Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_tc64_kernel launch");
 }
+template <bool OUT>
+vrwkv_status launch_tcf(const decay::TcParams& p, cudaStream_t s) {
+    static std::atomic<int> granted{0};
+    constexpr int smem = decay::tf_smem_bytes<OUT>();
+    const cudaError_t e = ensure_smem(decay::decay_attn_tcf_kernel<OUT>, granted, smem);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    decay::decay_attn_tcf_kernel<OUT><<<(unsigned)p.nitems, decay::kTfThreads, smem, s>>>(p);
+    return cuda_status(cudaGetLastError(), "decay_attn_tcf_kernel launch");
+}
+
 // Operands of the tensor cores as one bfloat16 each (P, K~) from this many
 // (sequence, token, head) rows on.  Their roundings, half a step each and
 // independent, then add to the output's own in quadrature: 1.41 times the
@@ -234,6 +247,10 @@ struct Launcher {
     const void* src[4]; // the tensors behind the maps, and their row strides
     long long ld[4];
 
+    const char* kernel(int D) const {
+        return !tc ? "decay_attn_kernel" : dtype == VRWKV_F32 ? "decay_attn_tcf_kernel"
+                   : D == 64 ? "decay_attn_tc64_kernel" : "decay_attn_tc_kernel";
+    }
     int map_of(const char* x, long long row) const {
         for (int i = 0; i < 4; ++i)
             if (src[i] == x && ld[i] == row) return i;
@@ -250,6 +267,7 @@ struct Launcher {
             t.mv[i] = map_of(p.pr[i].v, p.pr[i].ldv);
         }
         t.nitems = (int)ctas;
+        if (dtype == VRWKV_F32) return p.pr[0].out ? launch_tcf<true>(t, s) : launch_tcf<false>(t, s);
         return launch_tc_any(t, exact, s);
     }
 };
@@ -264,19 +282,23 @@ Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long*
     l.tc = tc_sizes(D, dtype) && !tc_disabled();
     l.t.wide_out = 1;
     for (int i = 0; i < no; ++i) {
-        l.tc = l.tc && aligned(outs[i], 16) && (D != 64 || encode_tokens(&l.t.omap[i], outs[i], H * D, B, T, H * D));
+        l.tc = l.tc && aligned(outs[i], 16);
         if (!aligned(outs[i], 32)) l.t.wide_out = 0;
     }
-    for (int i = 0; i < n && l.tc; ++i) l.tc = tma_ok(x[i], ld[i]);
+    const int es = elem_bytes(dtype);
+    for (int i = 0; i < n && l.tc; ++i) l.tc = rows16(x[i], ld[i], es);
     if (!l.tc) return l;
     l.t.err = device_error_word();
     l.t.wait_ns = wait_limit_ns();
     l.tc = l.t.err != nullptr;
+    if (dtype == VRWKV_F32) return l;  // reads and writes without TMA
     for (int i = 0; i < n && l.tc; ++i) {
         l.src[i] = x[i];
         l.ld[i] = ld[i];
         l.tc = encode_tokens(&l.t.map[i], x[i], ld[i], B, T, H * D);
     }
+    for (int i = 0; i < no && l.tc && D == 64; ++i)
+        l.tc = encode_tokens(&l.t.omap[i], outs[i], H * D, B, T, H * D);
     return l;
 }
 
@@ -329,7 +351,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     const long long lds[3] = {ldq, ldk, ldv};
     Launcher attn =
         make_launcher(dtype, srcs, lds, 3, dsts, 1, state_out != nullptr, B, T, H, D);
-    const Cut cut = plan(B, T, H, D, 1, attn.tc);
+    const Cut cut = plan(B, T, H, D, dtype, 1, attn.tc);
     decay::Params p = {};
     p.w = w;
     p.lengths = lengths;
@@ -377,7 +399,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     }
     pr.out = static_cast<char*>(out);
     st = attn.run(p, s);
-    if (st == VRWKV_OK) set_last_kernel(!attn.tc ? "decay_attn_kernel" : D == 64 ? "decay_attn_tc64_kernel" : "decay_attn_tc_kernel");
+    if (st == VRWKV_OK) set_last_kernel(attn.kernel(D));
     return st;
 }
 
@@ -416,7 +438,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     const long long lds[4] = {ldq, ldk, ldv, ldg};
     Launcher attn =
         make_launcher(dtype, srcs, lds, 4, dsts, 3, gstate_in != nullptr, B, T, H, D);
-    const Cut cut = plan(B, T, H, D, 3, attn.tc);
+    const Cut cut = plan(B, T, H, D, dtype, 3, attn.tc);
     decay::Params p = {};
     p.w = w;
     p.lengths = lengths;
@@ -483,7 +505,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     p.pr[1] = {V, G, Q, static_cast<char*>(gk), ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale, -1};
     p.pr[2] = {K, Q, G, static_cast<char*>(gv), ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale, -1};
     st = attn.run(p, s);
-    if (st == VRWKV_OK) set_last_kernel(!attn.tc ? "decay_attn_kernel" : D == 64 ? "decay_attn_tc64_kernel" : "decay_attn_tc_kernel");
+    if (st == VRWKV_OK) set_last_kernel(attn.kernel(D));
     return st;
 }
 

@@ -155,7 +155,8 @@ CASES = [
 
 
 def _kernel(dt, D):
-    return {64: "decay_attn_tc64_kernel", 128: "decay_attn_tc_kernel"}.get(D if dt == "bf16" else 0, "decay_attn_kernel")
+    return {("bf16", 64): "decay_attn_tc64_kernel", ("bf16", 128): "decay_attn_tc_kernel",
+            ("f32", 64): "decay_attn_tcf_kernel"}.get((dt, D), "decay_attn_kernel")
 
 
 @pytest.mark.parametrize("dt,B,T,H,D,packed,state,lens", CASES)
@@ -184,23 +185,35 @@ def test_backward(vk, dt, B, T, H, D, packed, state, lens):
         assert a is None or (a == b).all()
 
 
-def test_fp32_pipes_on_tensor_core_sizes(vk, monkeypatch):
-    """bfloat16 heads of 64 and 128 channels that TMA cannot read (rows that
-    start between 16-byte boundaries), and the same with the switch."""
+def test_any_size_kernel_on_tcgen05_sizes(vk, monkeypatch):
+    """Heads of 64 and 128 channels whose rows start between 16-byte
+    boundaries, and the same with the switch."""
     import torch
-    for D in (64, 128):
-        p = Problem("bf16", 2, 300, 1, D, 14, lens=[300, 140])
+    for dt, D in (("bf16", 64), ("bf16", 128), ("f32", 64)):
+        p = Problem(dt, 2, 300, 1, D, 14, lens=[300, 140])
         odd = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)  # noqa: E731
         p.q, p.k, p.v, p.g = (odd(t) for t in (p.q, p.k, p.v, p.g))
         p.check_fwd(*p.fwd(vk))
         assert vk.load_library().vrwkv_last_kernel() == b"decay_attn_kernel"
         p.check_bwd(p.bwd(vk))
         monkeypatch.setenv("VRWKV_DECAY_TC", "0")
-        p = Problem("bf16", 1, 1000, 1, D, 15)
+        p = Problem(dt, 1, 1000, 1, D, 15)
         p.check_fwd(*p.fwd(vk))
         assert vk.load_library().vrwkv_last_kernel() == b"decay_attn_kernel"
         p.check_bwd(p.bwd(vk))
         monkeypatch.delenv("VRWKV_DECAY_TC")
+
+
+@pytest.mark.parametrize("dt,B,T,H", [("f32", 60, 150, 4), ("f32", 2, 700, 3), ("f32", 1, 2100, 1)])
+def test_float32_heads_of_64(vk, dt, B, T, H):
+    """Decays on either side of the factored path's bound, several blocks, cuts."""
+    r = np.random.default_rng(18)
+    p = Problem(dt, B, T, H, 64, 18, True, True, [int(x) for x in r.integers(0, T + 1, B - 1)] + [T],
+                w=np.exp(np.linspace(-6, 0.3, H)))
+    p.check_fwd(*p.fwd(vk))
+    p.check_fwd(p.fwd(vk, want_state=False)[0], None)
+    p.check_bwd(p.bwd(vk))
+    vk.device_status()
 
 
 @pytest.mark.parametrize("B,T,H,state,ragged", [(60, 150, 7, False, False), (40, 196, 5, True, True), (90, 20, 4, True, True),
