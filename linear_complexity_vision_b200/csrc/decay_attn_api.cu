@@ -77,7 +77,7 @@ int padded_d(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 //   any size, DP = 32     9 (+ 0.6)        4 (+ 0.6)        3
 //             DP = 64     23 (+ 0.6)       9 (+ 0.6)        3
 //             DP = 128    45               18               1
-//   float32, D = 64       4.6              3.0              1
+//   float32, D = 64       7.3              4.5              1
 // Both sides measured: B = 1, T = 4096, 16 heads of 64, bfloat16: one segment
 // 56 us, eight 32 us; B = 8: one segment 62 us, two 130 us.
 struct Cut {
@@ -97,12 +97,12 @@ double pass_us(long long ctas, int units, const PassCost& c) {
     const long long per_sm = (ctas + sm_count() - 1) / sm_count(), rounds = per_sm / c.resident;
     const int rest = (int)(per_sm % c.resident);
     const double round = 1.0 + c.share * (c.resident - 1), last = rest ? 1.0 + c.share * (rest - 1) : 0.0;
-    return units * c.unit * (rounds * round + last) + 3.0;
+    return units * c.unit * (rounds * round + last) + 4.5;
 }
 
 Cut plan(int B, int T, int H, int D, vrwkv_dtype dtype, int nprob, bool tc) {
-    static const PassCost kOut[6] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}, {4.6, 0, 1}};
-    static const PassCost kState[6] = {{2.0, 0.5, 2}, {3.0, 0, 1}, {4, 0.6, 3}, {9, 0.6, 3}, {18, 0, 1}, {3.0, 0, 1}};
+    static const PassCost kOut[6] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}, {7.3, 0, 1}};
+    static const PassCost kState[6] = {{2.0, 0.5, 2}, {3.0, 0, 1}, {4, 0.6, 3}, {9, 0.6, 3}, {18, 0, 1}, {4.5, 0, 1}};
     const int kind = tc ? (dtype == VRWKV_F32 ? 5 : D == 64 ? 0 : 1) : (D <= 32 ? 2 : D <= 64 ? 3 : 4);
     const int units = (T + kSegUnit - 1) / kSegUnit;
     const long long heads = (long long)B * H;
@@ -183,13 +183,13 @@ bool encode_tokens(CUtensorMap* m, const void* x, long long ld, int B, int T, in
 // Rows that start on 16-byte boundaries (and a stride that TMA can hold).
 bool rows16(const void* x, long long ld, int es) { return aligned(x, 16) && ld * es % 16 == 0 && ld < (1LL << 36); }
 
-template <int D, bool OUT, int PIECES>
+template <int D, bool OUT, int PIECES, int PP>
 vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
     static std::atomic<int> granted{0};
     constexpr int smem = decay::tc_smem_bytes<D, OUT>();
-    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT, PIECES>, granted, smem);
+    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT, PIECES, PP>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    decay::decay_attn_tc_kernel<D, OUT, PIECES><<<ctas, decay::tc_threads<D>(), smem, s>>>(p);
+    decay::decay_attn_tc_kernel<D, OUT, PIECES, PP><<<ctas, decay::tc_threads<D>(), smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_tc_kernel launch");
 }
 template <int PIECES, int PP>
@@ -233,9 +233,12 @@ vrwkv_status launch_tc_any(decay::TcParams& p, bool exact, cudaStream_t s) {
         if (rounded) return exact ? launch_tc64<3, 1>(p, s) : launch_tc64<1, 1>(p, s);
         return exact ? launch_tc64<3, 2>(p, s) : launch_tc64<2, 2>(p, s);
     }
-    if (p.p.pr[0].out) return exact ? launch_tc<128, true, 3>(p, n, s) : launch_tc<128, true, 2>(p, n, s);
-    if (p.p.D == 64) return exact ? launch_tc<64, false, 3>(p, n, s) : launch_tc<64, false, 2>(p, n, s);
-    return exact ? launch_tc<128, false, 3>(p, n, s) : launch_tc<128, false, 2>(p, n, s);
+    if (p.p.pr[0].out) {
+        if (rounded) return exact ? launch_tc<128, true, 3, 1>(p, n, s) : launch_tc<128, true, 1, 1>(p, n, s);
+        return exact ? launch_tc<128, true, 3, 2>(p, n, s) : launch_tc<128, true, 2, 2>(p, n, s);
+    }
+    if (p.p.D == 64) return exact ? launch_tc<64, false, 3, 2>(p, n, s) : launch_tc<64, false, 2, 2>(p, n, s);
+    return exact ? launch_tc<128, false, 3, 2>(p, n, s) : launch_tc<128, false, 2, 2>(p, n, s);
 }
 
 // Launch p's problems; with `tc`, on the tensor cores with its maps.

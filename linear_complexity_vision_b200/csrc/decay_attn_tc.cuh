@@ -1,6 +1,6 @@
 // Multi-head decay attention on the 5th-generation tensor cores: the operator
 // of decay_attn.cuh (the same problems, segments and states) for bfloat16 and
-// heads of D = 64 or 128 channels, in chunks of 128 tokens.
+// heads of D = 128 (states: also 64) channels, in chunks of 128 tokens.
 //
 // Per chunk, with q, k, v tiles brought by TMA (128-byte swizzle) and X^T, the
 // state, in float32 registers:
@@ -12,15 +12,21 @@
 //   O += P v                          P from tensor memory, v as it lies in its tile
 //   U  = v^T K~                       K~ = e^{-w (..)} k as bfloat16 pieces
 //   X^T = e^{-w n} X^T + U            in registers
-// P and X end in bfloat16 outputs and are split in two, off by at most 2^-17
-// (half a step of a remainder below 2^-8).  So is K~ where no state leaves the
-// call; a state that does (PIECES = 3) is formed from three pieces, which hold
-// a float32 value exactly.
+// X ends in bfloat16 outputs and is split in two, off by at most 2^-17 (half a
+// step of a remainder below 2^-8).  P and K~ are split so too (PP, PIECES = 2)
+// or, on larger problems, rounded to one bfloat16 (1); a state that leaves the
+// call (PIECES = 3) is formed from three pieces, which hold a float32 value
+// exactly.
 //
-// Decays inside a chunk: a 32 x 32 block of P off the diagonal takes
-// e^{-w (t - s)} = e^{-w (t - s_end)} e^{-w (s_end - s)}, both exponents >= 0,
-// so fast decays underflow to 0 instead of overflowing; the diagonal block
-// takes it from a table by t - s.
+// Decays.  Where |w| <= 1/2, e^{-w (t - s)} = e^{-w (t - 63)} e^{-w (63 - s)}
+// stays within e^{+-32}: P takes the column's factor alone, the row's factor
+// multiplies the finished row of O, and X enters times e^{-64 w}, so that
+// O = q X and O += P v add up without a pass between them.  (A sum may then
+// grow to e^32 times the output before the last multiplication: outputs below
+// 1e24 are safe.)  For faster decays a 32 x 32 block of P off the diagonal takes
+// e^{-w (t - s_end)} e^{-w (s_end - s)}, both exponents >= 0, which underflow to
+// 0 instead of overflowing, the diagonal block takes a table by t - s, and
+// O = q X is scaled by rows in tensor memory.
 //
 // All working warps share every step; a warp's quarter of tensor memory (its
 // number mod 4) decides its rows, its warpgroup the columns.  One more warp
@@ -28,8 +34,10 @@
 // tensor pipe.  The tiles are loaded for the next chunk as soon as their last
 // readers are done: q and k (unless it holds the third piece) after A, O = q X
 // and K~, a whole chunk's work ahead; v after O += P v.
-// D = 64: 8 working warps, 96 KB of tiles, 256 tensor-memory columns, two CTAs
-// per SM, which fill each other's waits.  D = 128: 16 warps, 224 KB, one CTA.
+// D = 128: 16 working warps, 224 KB of tiles, 384 of the 512 tensor-memory
+// columns, one CTA per SM.  Without outputs (the states at the cuts of long
+// sequences) D = 64 runs here too: 8 warps, 64 KB, two CTAs per SM.  Its outputs
+// have a kernel of their own (decay_attn_tc64.cuh).
 //
 // Every wait is bounded: a wait that runs out records flag 8 in the device
 // error word, makes every warp leave its loop, waits (bounded) for copies and
@@ -43,6 +51,7 @@ namespace vrwkv {
 namespace decay {
 
 constexpr int kTcChunk = 128;
+constexpr float kTcFastW = 0.5f;
 constexpr unsigned kTcErr = 8u;
 
 struct TcParams {
@@ -72,8 +81,11 @@ struct alignas(1024) TcSmem {
     uint8_t q[OUT ? kTile : 1024];
     uint8_t xh[OUT ? kState : 1024], xl[OUT ? kState : 1024];  // X^T: rows v channel, K-major
     float pw[kTcChunk + 4];                             // e^{-w n}, n = 0 .. 128
-    float diag[64];  // scale_intra e^{-w d}, 0 for d < 0; d = t - s (s - t reversed) at 31 - d (31 + d)
-    float col[32];   // scale_intra e^{-w (31-i)}, reversed scale_intra e^{-w i}
+    // fast: scale_intra e^{-w (63 - s)} (reversed: s - 63); else [i] scale_intra e^{-w (31 - i)} (reversed: i)
+    float col[kTcChunk];
+    // fast: e^{-w (t - 63)} (reversed: 63 - t); else scale_intra e^{-w d}, 0 for d < 0, with d = t - s (s - t) at
+    // [31 - d] ([31 + d])
+    float row[kTcChunk];
     unsigned long long fa, fv, a, kt, u, pr, o, xr, of, drain;
     unsigned tmem;
     int abort;
@@ -98,13 +110,86 @@ __device__ __forceinline__ uint32_t split_bf16(float2& x) {
     return h;
 }
 
+// One 32 x 32 block of P, in the columns at taddr that hold the same block of A:
+// the thread's row (lane, in a quarter of the chunk's rows), columns 32 j .., d4
+// blocks back in (walked) time.  Two pieces: 16 columns of A become 8 of hi and 8
+// of lo; one: 32 become 16.  pw, col, row: the tables of TcSmem.
+template <int PP>
+__device__ __forceinline__ void p_block(uint32_t taddr, int j, int d4, bool fast, int rev, int lane, int m,
+                                        const float* pw, const float* col, const float* row) {
+    float all[32];
+    tc::tmem_ld32(taddr, all);
+    const float2 f = f2(fast ? 1.0f : pw[d4 == 0 ? 0 : rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);
+    const float* dg = row + 31 - lane;
+    const float* cl = fast ? col + 32 * j : col;
+    [[maybe_unused]] uint32_t packed[16];
+#pragma unroll
+    for (int g = 0; g < 32; g += 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = all[g + i];
+        if (d4 == 0 && !fast) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] *= dg[g + i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 c = *reinterpret_cast<const float4*>(cl + g + i);
+                float2 x = mul2(f2(v[i], v[i + 1]), f2(c.x, c.y));
+                float2 y = mul2(f2(v[i + 2], v[i + 3]), f2(c.z, c.w));
+                if (!fast) {
+                    x = mul2(x, f);
+                    y = mul2(y, f);
+                }
+                v[i] = x.x;
+                v[i + 1] = x.y;
+                v[i + 2] = y.x;
+                v[i + 3] = y.y;
+            }
+            if (d4 == 0 && PP == 2) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (rev ? g + i < lane : g + i > lane) v[i] = 0.f;
+            }
+        }
+        if (32 * j + g + 16 > m) {  // columns past the chunk's tokens
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (32 * j + g + i >= m) v[i] = 0.f;
+        }
+        if constexpr (PP == 2) {
+            uint32_t out[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float2 x = f2(v[2 * i], v[2 * i + 1]);
+                out[i] = split_bf16(x);
+                out[8 + i] = pack_bf16(x);
+            }
+            tc::tmem_st16(taddr + g, out);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) packed[g / 2 + i] = pack_bf16(f2(v[2 * i], v[2 * i + 1]));
+        }
+    }
+    if constexpr (PP == 1) {
+        if (d4 == 0 && fast) {      // bits of the columns in the row's future
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int past = rev ? 2 * i + 1 - lane : lane - 2 * i;  // >= 1: both stay, 0: the nearer
+                packed[i] &= past > 0 ? 0xffffffffu : past < 0 ? 0u : rev ? 0xffff0000u : 0x0000ffffu;
+            }
+        }
+        tc::tmem_st16(taddr, packed);
+    }
+}
+
 __device__ __forceinline__ void st_global_32(char* p, const uint32_t (&r)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
-template <int D, bool OUT, int PIECES>
+template <int D, bool OUT, int PIECES, int PP>
 __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     decay_attn_tc_kernel(const __grid_constant__ TcParams P) {
     using Sm = TcSmem<D, OUT>;
@@ -146,11 +231,18 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tc::tmem_alloc(&S.tmem, kCols);
-    for (int i = tid; i <= C; i += kThreads) S.pw[i] = decay_pow(w, i);
-    if (OUT && tid >= 64 && tid < 128) {
-        const int d = rev ? tid - 64 - 31 : 31 - (tid - 64);
-        S.diag[tid - 64] = d < 0 ? 0.f : decay_pow(w, d) * pr.scale_intra;
-        if (tid < 96) S.col[tid - 64] = decay_pow(w, rev ? tid - 64 : 31 - (tid - 64)) * pr.scale_intra;
+    const DecayBase base = decay_base(w);
+    const bool fast = fabsf(w) <= kTcFastW;
+    for (int i = tid; i <= C; i += kThreads) S.pw[i] = decay_pow(base, i);
+    if (OUT && tid < C) {
+        if (fast) {
+            S.col[tid] = decay_pow(base, rev ? tid - 63 : 63 - tid) * pr.scale_intra;
+            S.row[tid] = decay_pow(base, rev ? 63 - tid : tid - 63);
+        } else {
+            const int d = rev ? tid - 31 : 31 - tid;
+            if (tid < 32) S.col[tid] = decay_pow(base, rev ? tid : 31 - tid) * pr.scale_intra;
+            if (tid < 64) S.row[tid] = d < 0 ? 0.f : decay_pow(base, d) * pr.scale_intra;
+        }
     }
 
     volatile int* abort = &S.abort;
@@ -205,8 +297,9 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < NX; ++i) X[i] = 0.f;
     }
-    // X^T as operands: row jr, 16-byte piece c of 64 channels at piece c ^ (jr & 7)
-    auto store_x = [&]() {
+    // X^T as operands of a chunk of m tokens: row jr, 16-byte piece c of 64 channels at piece c ^ (jr & 7)
+    auto store_x = [&](int m) {
+        const float2 f = f2(fast ? decay_pow(base, rev ? m - 64 : 64) * pr.scale_inter : 1.0f);
 #pragma unroll
         for (int i = 0; i < NX; i += 8) {
             const int c = c0 + i;
@@ -214,7 +307,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float2 x = f2(X[i + 2 * e], X[i + 2 * e + 1]);
+                float2 x = mul2(f2(X[i + 2 * e], X[i + 2 * e + 1]), f);
                 hi[e] = split_bf16(x);
                 lo[e] = pack_bf16(x);
             }
@@ -224,7 +317,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         tc::fence_async_smem();
         arrive_warp(S.xr);
     };
-    if (OUT && has_in && !issuer) store_x();
+    if (OUT && has_in && !issuer && nchunk > 0) store_x(min(C, n - first(0)));
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -293,7 +386,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 if (OUT && !wait_warp(S.a, ci)) break;
                 if (tc::elect_one()) {
                     load_q(ci + 1);
-                    if (PIECES == 2) load_k(ci + 1);
+                    if (PIECES < 3) load_k(ci + 1);
                 }
                 ++loads_a;
                 __syncwarp();
@@ -307,9 +400,9 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
 #pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            tc::mma_ts(tmem + kColO, tmem + 16 * k + 8 * half, db + 128 * k, kIdP,
-                                       k + half > 0 ? 1u : acc);
+                        for (int half = 0; half < PP; ++half)
+                            tc::mma_ts(tmem + kColO, tmem + (PP == 2 ? 16 * k + 8 * half : 32 * (k / 2) + 8 * (k % 2)),
+                                       db + 128 * k, kIdP, k + half > 0 ? 1u : acc);
                     tc::commit(&S.o);
                 }
                 __syncwarp();
@@ -378,12 +471,12 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                     if (PIECES == 3) {
                         mi[e] = split_bf16(y);
                         lo[e] = pack_bf16(y);
-                    } else {
+                    } else if (PIECES == 2) {
                         mi[e] = pack_bf16(y);
                     }
                 }
                 *reinterpret_cast<uint4*>(S.kh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(S.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                if (PIECES >= 2) *reinterpret_cast<uint4*>(S.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
                 if (PIECES == 3) *reinterpret_cast<uint4*>(S.k + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
@@ -398,49 +491,12 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 const int d4 = NWG == 4 ? wg : (wg == 0 ? 3 * jj : 1 + jj);
                 const int j = rev ? (quad + d4) & 3 : (quad - d4) & 3;
                 if (d4 > wq || 32 * j >= m) {           // before the sequence's start, or past the chunk's end
-                    tc::tmem_zero<32>(lanes + 32 * j);
+                    tc::tmem_zero<16 * PP>(lanes + 32 * j);
                     continue;
                 }
-                const float2 f = f2(S.pw[d4 == 0 ? 0 : rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);
-                const float* dg = S.diag + 31 - lane;
-                float all[32];
-                tc::tmem_ld32(lanes + 32 * j, all);
-#pragma unroll
-                for (int g = 0; g < 32; g += 16) {      // 16 columns become 8 of hi and 8 of lo
-                    float v[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = all[g + i];
-                    if (d4 == 0) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] *= dg[g + i];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 c = *reinterpret_cast<const float4*>(S.col + g + i);
-                            const float2 x = mul2(f2(v[i], v[i + 1]), mul2(f2(c.x, c.y), f));
-                            const float2 y = mul2(f2(v[i + 2], v[i + 3]), mul2(f2(c.z, c.w), f));
-                            v[i] = x.x;
-                            v[i + 1] = x.y;
-                            v[i + 2] = y.x;
-                            v[i + 3] = y.y;
-                        }
-                    }
-                    if (32 * j + g + 16 > m) {          // columns past the chunk's tokens
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (32 * j + g + i >= m) v[i] = 0.f;
-                    }
-                    uint32_t out[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 x = f2(v[2 * i], v[2 * i + 1]);
-                        out[i] = split_bf16(x);
-                        out[8 + i] = pack_bf16(x);
-                    }
-                    tc::tmem_st16(lanes + 32 * j + g, out);
-                }
+                p_block<PP>(lanes + 32 * j, j, d4, fast, rev, lane, m, S.pw, S.col, S.row);
             }
-            if (with_x) {
+            if (!fast && with_x) {
                 const int row = quad * 32 + lane;
                 const float2 f = f2(S.pw[max(rev ? m - 1 - row : row, 0) + e0] * pr.scale_inter);
 #pragma unroll
@@ -475,7 +531,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 X[i + 1] = x.y;
             }
             tc::fence_before();
-            if (OUT && more) store_x();
+            if (OUT && more) store_x(min(C, n - first(ci + 1)));
         }
         if (OUT) {
             if (!wait_warp(S.o, ci)) break;
@@ -486,12 +542,13 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
             tc::fence_before();
             arrive_warp(S.of);
             if (row < m) {
+                const float2 f = f2(fast ? S.row[row] : 1.0f);
                 char* dst = pr.out + ((((size_t)b * p.T + t0 + a + row) * p.H + h) * D + wg * 32) * 2;
 #pragma unroll
                 for (int i = 0; i < 32; i += 16) {
                     uint32_t o[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = pack_bf16(f2(v[i + 2 * e], v[i + 2 * e + 1]));
+                    for (int e = 0; e < 8; ++e) o[e] = pack_bf16(mul2(f2(v[i + 2 * e], v[i + 2 * e + 1]), f));
                     if (P.wide_out) {
                         st_global_32(dst + 2 * i, o);
                     } else {

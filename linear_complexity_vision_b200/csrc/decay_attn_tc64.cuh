@@ -8,14 +8,6 @@
 // serial: four warps keep it in registers, add each chunk's U in turn and hand
 // the operands of O = q X to the stream whose chunk is next.
 //
-// Decays.  Where |w| <= 1/2, e^{-w (t - s)} = e^{-w (t - 63)} e^{-w (63 - s)}
-// stays within e^{+-32}: P takes the column's factor alone, the row's factor
-// multiplies the finished row of O, and X enters times e^{-64 w}, so that
-// O = q X and O += P v add up without a pass between them.  (A sum may then
-// grow to e^32 times the output before the last multiplication: outputs below
-// 1e24 are safe.)  Faster decays take the block-wise factors of
-// decay_attn_tc.cuh and scale O = q X by rows in tensor memory.
-//
 // Roles (704 threads): warps 0-7 and 8-15 the workers of streams 0 and 1,
 // warps 16-19 the state, warps 20-21 the issuers.  512 tensor-memory columns:
 // per stream A / P 128, O 64, U 64.  Bounded waits as in decay_attn_tc.cuh.
@@ -33,13 +25,12 @@ namespace vrwkv {
 namespace decay {
 
 constexpr int kT64Threads = 704;
-constexpr float kT64FastW = 0.5f;
 
 struct alignas(1024) T64Smem {
     struct Tables {                  // of one work item
         float pw[kTcChunk + 4];      // e^{-w n}, n = 0 .. 128
-        float col[kTcChunk];         // fast: scale_intra e^{-w (63 - s)} (reversed: s - 63); else as TcSmem's col
-        float row[kTcChunk];         // fast: e^{-w (t - 63)} (reversed: 63 - t); else [31 + d] as TcSmem's diag
+        float col[kTcChunk];         // as TcSmem's
+        float row[kTcChunk];
     };
     struct Stream {
         uint8_t q[16384], k[16384], v[16384], kh[16384], km[16384];
@@ -97,7 +88,7 @@ struct T64Item {
     __device__ __forceinline__ long long state_at(const Params& p) const {
         return (((long long)b * p.H + h) * p.nseg + seg) * 64 * 64;
     }
-    __device__ __forceinline__ bool fast() const { return fabsf(w) <= kT64FastW; }
+    __device__ __forceinline__ bool fast() const { return fabsf(w) <= kTcFastW; }
 };
 
 // A stream's walk over its chunks: every second one of the items' chunks in
@@ -267,74 +258,10 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 const int d4 = wg == 0 ? 3 * jj : 1 + jj;
                 const int j = rev ? (quad + d4) & 3 : (quad - d4) & 3;
                 if (d4 > wq || 32 * j >= m) {           // before the sequence's start, or past the chunk's end
-                    if (PP == 2) tc::tmem_zero<32>(lanes + 32 * j);
-                    else tc::tmem_zero<16>(lanes + 32 * j);
+                    tc::tmem_zero<16 * PP>(lanes + 32 * j);
                     continue;
                 }
-                float all[32];
-                tc::tmem_ld32(lanes + 32 * j, all);
-                const float2 f = f2(fast ? 1.0f : N.pw[d4 == 0 ? 0 : rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);
-                const float* dg = N.row + 31 - lane;
-                const float* cl = fast ? N.col + 32 * j : N.col;
-                [[maybe_unused]] uint32_t packed[16];
-#pragma unroll
-                for (int g = 0; g < 32; g += 16) {      // 16 columns become 8 of hi and 8 of lo
-                    float v[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = all[g + i];
-                    if (d4 == 0 && !fast) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] *= dg[g + i];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 c = *reinterpret_cast<const float4*>(cl + g + i);
-                            float2 x = mul2(f2(v[i], v[i + 1]), f2(c.x, c.y));
-                            float2 y = mul2(f2(v[i + 2], v[i + 3]), f2(c.z, c.w));
-                            if (!fast) {
-                                x = mul2(x, f);
-                                y = mul2(y, f);
-                            }
-                            v[i] = x.x;
-                            v[i + 1] = x.y;
-                            v[i + 2] = y.x;
-                            v[i + 3] = y.y;
-                        }
-                        if (d4 == 0 && PP == 2) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (rev ? g + i < lane : g + i > lane) v[i] = 0.f;
-                        }
-                    }
-                    if (32 * j + g + 16 > m) {          // columns past the chunk's tokens
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (32 * j + g + i >= m) v[i] = 0.f;
-                    }
-                    if constexpr (PP == 2) {
-                        uint32_t out[16];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float2 x = f2(v[2 * i], v[2 * i + 1]);
-                            out[i] = split_bf16(x);
-                            out[8 + i] = pack_bf16(x);
-                        }
-                        tc::tmem_st16(lanes + 32 * j + g, out);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) packed[g / 2 + i] = pack_bf16(f2(v[2 * i], v[2 * i + 1]));
-                    }
-                }
-                if constexpr (PP == 1) {
-                    if (d4 == 0 && fast) {              // bits of the columns in the row's future
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int past = rev ? 2 * i + 1 - lane : lane - 2 * i;  // >= 1: both stay, 0: the nearer
-                            packed[i] &= past > 0 ? 0xffffffffu : past < 0 ? 0u : rev ? 0xffff0000u : 0x0000ffffu;
-                        }
-                    }
-                    tc::tmem_st16(lanes + 32 * j, packed);
-                }
+                p_block<PP>(lanes + 32 * j, j, d4, fast, rev, lane, m, N.pw, N.col, N.row);
             }
             const int row = quad * 32 + lane;
             if (!fast && cu.with_x()) {

@@ -38,7 +38,6 @@ namespace vrwkv {
 namespace decay {
 
 constexpr int kTfThreads = 544;
-constexpr float kTfFastW = 0.5f;
 
 template <bool OUT>
 struct alignas(1024) TfSmem {
@@ -74,7 +73,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     const bool issuer = warp == NW;
     const float w = __ldg(p.w + h);
     const DecayBase base = decay_base(w);
-    const bool fast = fabsf(w) <= kTfFastW && pr.scale_intra != 0.f;
+    const bool fast = fabsf(w) <= kTcFastW && pr.scale_intra != 0.f;
     const int n_seq = seq_tokens(p.lengths, b, p.T);
     const int t0 = seg * p.seg_tokens;
     const int n = seg_count(n_seq, seg, p.seg_tokens);

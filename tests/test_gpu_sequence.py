@@ -77,7 +77,7 @@ def _ops(D, T):
     return 2 * (2 * D + 128 + T) + 16 + 104
 
 
-TC_SIZES = (64,)
+TC_SIZES = (64, 128)
 
 
 class Problem:
@@ -230,6 +230,19 @@ def test_more_heads_than_sms(vk, B, T, H, state, ragged):
     got = p.bwd(vk)
     vk.device_status()
     p.check_bwd(got)
+
+
+@pytest.mark.parametrize("B,T,H,lens", [(20, 300, 2, True), (2, 2100, 2, False)])
+def test_heads_of_128(vk, B, T, H, lens):
+    """From 8192 rows on, decays on either side of the factored path's bound."""
+    r = np.random.default_rng(19)
+    p = Problem("bf16", B, T, H, 128, 19, True, True, [int(x) for x in r.integers(0, T + 1, B)] if lens else None,
+                w=np.exp(np.linspace(-4, 0.3, H)))
+    assert p.rounded
+    p.check_fwd(*p.fwd(vk))
+    p.check_fwd(p.fwd(vk, want_state=False)[0], None)
+    p.check_bwd(p.bwd(vk))
+    vk.device_status()
 
 
 @pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 40)])
