@@ -480,8 +480,8 @@ __global__ void __launch_bounds__(256) decay_chain_kernel(const ChainParams p) {
 // Bound by the state's bytes (read and written once).  A CTA takes a slab of
 // 32 columns of one head's state: independent of the other slabs, 128-byte
 // rows, and enough CTAs at batch 1.  Thread (r, c4): rows r, r + RT, .. and
-// the 4 columns c4; the columns' partial sums over the rows meet in shared
-// memory.
+// the 4 columns c4, NP passes over the rows; the columns' partial sums over the
+// rows meet in shared memory.
 // ---------------------------------------------------------------------------
 struct StepParams {
     const char* q;          // (B, H*D), row strides in elements
@@ -504,7 +504,7 @@ constexpr int kStepCols = 32;                       // columns of a CTA
 constexpr int kStepRows = kStepThreads / (kStepCols / 4);  // rows of one pass
 constexpr int kStepMaxD = 128;
 
-template <typename IO>
+template <typename IO, int NP>
 __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepParams p) {
     __shared__ float sq[kStepMaxD], sk[kStepMaxD];
     __shared__ float4 part[kStepRows / 4][kStepCols / 4];  // one row per warp
@@ -514,7 +514,6 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepPara
     const int slot = p.slots ? __ldg(p.slots + b) : b;
     const bool in_range = slot >= 0 && slot < p.N;
     constexpr int es = sizeof(IO);
-    constexpr int NP = kStepMaxD / kStepRows;       // passes over the rows
     float* S = p.state + ((size_t)(in_range ? slot : 0) * p.H + h) * D * D;
 
     float4 x[NP];
@@ -525,7 +524,7 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepPara
         if (in_range && i < D && j < D) {
             const float* s = S + (size_t)i * D + j;
             if (p.vec) {
-                x[m] = *reinterpret_cast<const float4*>(s);
+                x[m] = __ldcs(reinterpret_cast<const float4*>(s));
             } else {
                 x[m].x = s[0];
                 if (j + 1 < D) x[m].y = s[1];
@@ -569,7 +568,7 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepPara
             if (j < D) {
                 float* s = S + (size_t)i * D + j;
                 if (p.vec) {
-                    *reinterpret_cast<float4*>(s) = x[m];
+                    __stcs(reinterpret_cast<float4*>(s), x[m]);
                 } else {
                     s[0] = x[m].x;
                     if (j + 1 < D) s[1] = x[m].y;

@@ -556,8 +556,14 @@ vrwkv_status vrwkv_decay_attn_step(const void* q, const void* k, const void* v, 
     if (!p.err) return fail(VRWKV_ERR_CUDA, "cannot locate the device error word");
     const dim3 grid((unsigned)B, (unsigned)H, (unsigned)((D + decay::kStepCols - 1) / decay::kStepCols));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == VRWKV_F32) decay::decay_step_kernel<float><<<grid, decay::kStepThreads, 0, s>>>(p);
-    else decay::decay_step_kernel<__nv_bfloat16><<<grid, decay::kStepThreads, 0, s>>>(p);
+    auto launch = [&](auto io) {
+        using IO = decltype(io);
+        if (D <= 32) decay::decay_step_kernel<IO, 2><<<grid, decay::kStepThreads, 0, s>>>(p);
+        else if (D <= 64) decay::decay_step_kernel<IO, 4><<<grid, decay::kStepThreads, 0, s>>>(p);
+        else decay::decay_step_kernel<IO, 8><<<grid, decay::kStepThreads, 0, s>>>(p);
+    };
+    if (dtype == VRWKV_F32) launch(float{});
+    else launch(__nv_bfloat16{});
     st = cuda_status(cudaGetLastError(), "decay_step_kernel launch");
     if (st == VRWKV_OK) set_last_kernel("decay_step_kernel");
     return st;

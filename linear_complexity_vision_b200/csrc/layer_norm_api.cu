@@ -54,8 +54,8 @@ LnBwdPlan ln_bwd_plan(long long rows, int C, int es, bool vec) {
     if (pl.vec && (vectors + 31) / 32 * (16 / es) <= 32) {
         pl.vpl = (vectors + 31) / 32;
         pl.threads = 32 * kLnBwdWarps;
-        // three CTAs of at most 168 registers a thread stay resident
-        pl.grid = (int)std::min<long long>((rows + kLnBwdWarps - 1) / kLnBwdWarps, 3LL * sm_count());
+        const int ctas = es == 4 ? ln_bwd_ctas<float>(pl.vpl) : ln_bwd_ctas<__nv_bfloat16>(pl.vpl);  // resident on an SM
+        pl.grid = (int)std::min<long long>((rows + kLnBwdWarps - 1) / kLnBwdWarps, (long long)ctas * sm_count());
         return pl;
     }
     pl.nv = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 8;

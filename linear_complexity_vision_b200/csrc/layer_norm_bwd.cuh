@@ -3,12 +3,18 @@
 //   ggamma = sum_rows gy xh,  gbeta = sum_rows gy.
 // Bound by its bytes (x and gy read, gx written once).  Rows of at most 32
 // channels a lane go to a warp each (layer_norm_bwd_warp_kernel): a row's two
-// sums then cost 10 shuffles and no barrier, and the next row is on its way
-// while one is worked on.  Wider rows, or rows that are not made of aligned
-// 16-byte vectors, go to a CTA each.  Either way a thread keeps the same
-// channels of every row it visits, so their ggamma and gbeta stay in its
-// registers; each CTA leaves one partial row of them, and
-// layer_norm_wgrad_kernel adds the partial rows in a fixed order.
+// sums then cost 10 shuffles and no barrier, and the next row is on its way in
+// registers while one is worked on.  Measured in a graph, both kernels of the
+// call: 32768 x 1024 bfloat16 44.3 us, 12544 x 768 bfloat16 19.6, 6272 x 384
+// float32 10.1, 32768 x 1024 float32 73.1 us (5.5 TB/s).  The same with the rows
+// on their way in a ring of shared memory (bulk copies, four CTAs an SM): 46.7,
+// 21.2, 11.0 and 78.9; with three CTAs and spills for wide float32 rows 126 us.
+// bfloat16 is bound by its arithmetic beside the bytes: each element is unpacked
+// twice and takes eight FP32 operations, paired.  Wider rows, or rows that are
+// not made of aligned 16-byte vectors, go to a CTA each.  Either way a thread
+// keeps the same channels of every row it visits, so their ggamma and gbeta stay
+// in its registers; each CTA leaves one partial row of them, and
+// layer_norm_wgrad_kernel adds those rows in a fixed order.
 #pragma once
 
 #include "common.cuh"
@@ -44,20 +50,38 @@ struct LnVec {
     }
 };
 
+// The N channels of a 16-byte vector as float pairs (paired FP32 instructions).
+__device__ __forceinline__ void ln_pairs(const uint4& r, float2 (&f)[2], float) {
+    f[0] = f2(__uint_as_float(r.x), __uint_as_float(r.y));
+    f[1] = f2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+__device__ __forceinline__ void ln_pairs(const uint4& r, float2 (&f)[4], __nv_bfloat16) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+
 constexpr int kLnBwdWarps = 4;
+// CTAs of an SM, by registers: the row at hand, the next one and the sums of
+// gradients are 16 VPL + 2 E of them, and there are about 40 others.
+template <typename IO>
+constexpr int ln_bwd_ctas(int vpl) {
+    const int regs = 40 + 16 * vpl + 2 * vpl * Vec16<IO>::N, fit = 65536 / (32 * kLnBwdWarps * regs);
+    return fit < 6 ? fit : 6;
+}
 
 template <typename IO, int VPL>
-__global__ void __launch_bounds__(32 * kLnBwdWarps, 3) layer_norm_bwd_warp_kernel(const LayerNormBwdParams p) {
+__global__ void __launch_bounds__(32 * kLnBwdWarps, ln_bwd_ctas<IO>(VPL)) layer_norm_bwd_warp_kernel(const LayerNormBwdParams p) {
     using V = Vec16<IO>;
-    constexpr int N = V::N, E = VPL * N;  // channels of a lane: vectors lane + 32 k
+    constexpr int N = V::N, N2 = N / 2, E = VPL * N;  // channels of a lane: vectors lane + 32 k
     extern __shared__ __align__(16) float sg[];  // gamma, then the CTA's partial rows: max(1, 2) * C floats
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nv = p.C / N;
     for (int c = tid; c < p.C; c += 32 * kLnBwdWarps) sg[c] = __ldg(p.g + c);
     __syncthreads();
-    float dg[E], db[E];
+    float2 dg[E / 2], db[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) dg[e] = db[e] = 0.f;
+    for (int e = 0; e < E / 2; ++e) dg[e] = db[e] = f2(0.f);
     const float invC = 1.0f / (float)p.C;
     const size_t rowb = (size_t)p.C * sizeof(IO);
     const long long step = (long long)gridDim.x * kLnBwdWarps;
@@ -87,35 +111,42 @@ __global__ void __launch_bounds__(32 * kLnBwdWarps, 3) layer_norm_bwd_warp_kerne
         }
         const float mean = nmean, rs = nrs;
         if (row + step < p.rows) fetch(row + step);
-        float a = 0.f, b = 0.f;
+        float2 a2 = f2(0.f), b2 = f2(0.f);
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             const int v = lane + 32 * k;
-            float x[N], y[N];
-            V::unpack(cx[k], x);
-            V::unpack(cg[k], y);
             if (v >= nv) continue;
+            const float2* gg = reinterpret_cast<const float2*>(sg + v * N);
+            float2 x[N2], y[N2];
+            ln_pairs(cx[k], x, IO{});
+            ln_pairs(cg[k], y, IO{});
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float xh = (x[e] - mean) * rs, d = sg[v * N + e] * y[e];
-                a += d;
-                b = fmaf(d, xh, b);
-                dg[k * N + e] = fmaf(y[e], xh, dg[k * N + e]);
-                db[k * N + e] += y[e];
+            for (int e = 0; e < N2; ++e) {
+                const float2 xh = mul2(add2(x[e], f2(-mean)), f2(rs)), d = mul2(gg[e], y[e]);
+                a2 = add2(a2, d);
+                b2 = fma2(d, xh, b2);
+                dg[k * N2 + e] = fma2(y[e], xh, dg[k * N2 + e]);
+                db[k * N2 + e] = add2(db[k * N2 + e], y[e]);
             }
         }
-        a = warp_sum(a) * invC;
-        b = warp_sum(b) * invC;
+        const float a = warp_sum(a2.x + a2.y) * invC, b = warp_sum(b2.x + b2.y) * invC;
+        // rs (g y - mean(d) - (x - mean) rs mean(d xh)), the row's constants joined
+        const float c1 = -rs * rs * b, c0 = -rs * a;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             const int v = lane + 32 * k;
             if (v >= nv) continue;
-            float x[N], y[N], o[N];
-            V::unpack(cx[k], x);
-            V::unpack(cg[k], y);
+            const float2* gg = reinterpret_cast<const float2*>(sg + v * N);
+            float2 x[N2], y[N2];
+            float o[N];
+            ln_pairs(cx[k], x, IO{});
+            ln_pairs(cg[k], y, IO{});
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                o[e] = rs * (fmaf(sg[v * N + e], y[e], -a) - (x[e] - mean) * rs * b);
+            for (int e = 0; e < N2; ++e) {
+                const float2 r = fma2(add2(x[e], f2(-mean)), f2(c1), fma2(mul2(f2(rs), gg[e]), y[e], f2(c0)));
+                o[2 * e] = r.x;
+                o[2 * e + 1] = r.y;
+            }
             reinterpret_cast<uint4*>(p.gx + row * rowb)[v] = V::pack(o);
         }
     }
@@ -131,8 +162,9 @@ __global__ void __launch_bounds__(32 * kLnBwdWarps, 3) layer_norm_bwd_warp_kerne
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const int c = v * N + e;
-                sg[c] = dg[k * N + e] + (w ? sg[c] : 0.f);
-                sg[p.C + c] = db[k * N + e] + (w ? sg[p.C + c] : 0.f);
+                const float2 g2 = dg[k * N2 + e / 2], b2 = db[k * N2 + e / 2];
+                sg[c] = (e & 1 ? g2.y : g2.x) + (w ? sg[c] : 0.f);
+                sg[p.C + c] = (e & 1 ? b2.y : b2.x) + (w ? sg[p.C + c] : 0.f);
             }
         }
     }
