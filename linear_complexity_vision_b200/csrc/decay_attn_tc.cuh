@@ -33,10 +33,11 @@
 // issues loads and MMAs and works on nothing else, since issuing waits for the
 // tensor pipe.  The tiles are loaded for the next chunk as soon as their last
 // readers are done: q and k (unless it holds the third piece) after A, O = q X
-// and K~, a whole chunk's work ahead; v after O += P v.
+// and K~, a whole chunk's work ahead; v after O += P v (without outputs there is
+// room for two tiles of v and for the third piece: loads are two chunks ahead).
 // D = 128: 16 working warps, 224 KB of tiles, 384 of the 512 tensor-memory
 // columns, one CTA per SM.  Without outputs (the states at the cuts of long
-// sequences) D = 64 runs here too: 8 warps, 64 KB, two CTAs per SM.  Its outputs
+// sequences) D = 64 runs here too: 8 warps, 98 KB, two CTAs per SM.  Its outputs
 // have a kernel of their own (decay_attn_tc64.cuh).
 //
 // Every wait is bounded: a wait that runs out records flag 8 in the device
@@ -77,8 +78,8 @@ struct alignas(1024) TcSmem {
     static constexpr int kSub = D / 64;                 // 64-channel subtiles of a tile
     static constexpr int kTile = kSub * 128 * 128;      // bytes of a token tile
     static constexpr int kState = kSub * D * 128;       // bytes of a state operand
-    uint8_t k[kTile], v[kTile], kh[kTile], km[kTile];
-    uint8_t q[OUT ? kTile : 1024];
+    uint8_t k[kTile], v[OUT ? 1 : 2][kTile], kh[kTile], km[kTile];
+    uint8_t q[kTile];                                   // without outputs: K~'s third piece
     uint8_t xh[OUT ? kState : 1024], xl[OUT ? kState : 1024];  // X^T: rows v channel, K-major
     float pw[kTcChunk + 4];                             // e^{-w n}, n = 0 .. 128
     // fast: scale_intra e^{-w (63 - s)} (reversed: s - 63); else [i] scale_intra e^{-w (31 - i)} (reversed: i)
@@ -86,7 +87,7 @@ struct alignas(1024) TcSmem {
     // fast: e^{-w (t - 63)} (reversed: 63 - t); else scale_intra e^{-w d}, 0 for d < 0, with d = t - s (s - t) at
     // [31 - d] ([31 + d])
     float row[kTcChunk];
-    unsigned long long fa, fv, a, kt, u, pr, o, xr, of, drain;
+    unsigned long long fa, fv[2], a, kt, u, pr, o, xr, of, drain;
     unsigned tmem;
     int abort;
 };
@@ -192,11 +193,12 @@ __device__ __forceinline__ void st_global_32(char* p, const uint32_t (&r)[8]) {
 template <int D, bool OUT, int PIECES, int PP>
 __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     decay_attn_tc_kernel(const __grid_constant__ TcParams P) {
+    static_assert(D == 128 || !OUT, "outputs of D = 64 have a kernel of their own");
     using Sm = TcSmem<D, OUT>;
     constexpr int C = kTcChunk, SUB = Sm::kSub, SUBB = 128 * 128, kThreads = tc_threads<D>();
     constexpr int NWG = kThreads / 128, NW = 4 * NWG, kWork = 32 * NW;
     constexpr uint32_t kColO = 128, kColU = OUT ? 128 + D : 0;
-    constexpr uint32_t kCols = OUT ? (D == 64 ? 256 : 512) : D;
+    constexpr uint32_t kCols = OUT ? 512 : D;
     constexpr int NX = D * D / kWork;                   // state values of a thread
     extern __shared__ __align__(1024) char smem_raw[];
     Sm& S = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -218,7 +220,8 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
 
     if (tid == 0) {
         tc::mbar_init(&S.fa, 1);
-        tc::mbar_init(&S.fv, 1);
+        tc::mbar_init(&S.fv[0], 1);
+        tc::mbar_init(&S.fv[1], 1);
         tc::mbar_init(&S.a, 1);
         tc::mbar_init(&S.kt, NW);
         tc::mbar_init(&S.u, 1);
@@ -259,7 +262,11 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     };
     // chunk ci of the walk: its first token in the segment
     auto first = [&](int ci) { return (rev ? nchunk - 1 - ci : ci) * C; };
-    const uint32_t sq = tc::smem_u32(S.q), sk = tc::smem_u32(S.k), sv = tc::smem_u32(S.v);
+    constexpr int NV = OUT ? 1 : 2;                     // tiles of v
+    const uint32_t sq = tc::smem_u32(S.q), sk = tc::smem_u32(S.k);
+    auto sv = [&](int ci) { return tc::smem_u32(S.v[ci % NV]); };
+    uint8_t* third = OUT ? S.k : S.q;                   // of K~'s pieces
+    const uint32_t s3 = tc::smem_u32(third);
     const uint32_t skh = tc::smem_u32(S.kh), skm = tc::smem_u32(S.km), sxh = tc::smem_u32(S.xh), sxl = tc::smem_u32(S.xl);
     auto load = [&](uint32_t dst, int map, int ci, unsigned long long* bar) {
 #pragma unroll
@@ -274,13 +281,14 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     };
     auto load_k = [&](int ci) { load(sk, P.mk[prob], ci, &S.fa); };
     auto load_v = [&](int ci) {
-        tc::mbar_expect_tx(&S.fv, Sm::kTile);
-        load(sv, P.mv[prob], ci, &S.fv);
+        tc::mbar_expect_tx(&S.fv[ci % NV], Sm::kTile);
+        load(sv(ci), P.mv[prob], ci, &S.fv[ci % NV]);
     };
     if (issuer && nchunk > 0 && tc::elect_one()) {
         load_q(0);
         load_k(0);
         load_v(0);
+        if (!OUT && nchunk > 1) load_v(1);
     }
 
     // X: row jr of X^T (a v channel), columns c0 .. (k channels).  For D = 64
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     constexpr uint32_t kIdP = tc::idesc_bf16(128, D, false, true);
     constexpr uint32_t kIdU = tc::idesc_bf16(128, D, true, true);
     if (issuer) {
-        int loads_a = 1, loads_v = 1;  // phases of fa and fv begun, if there are tokens
+        int loads_a = 1, loads_v = OUT ? 1 : 2;  // loads of k and v begun, if there are as many chunks
         bool issued = false;
         for (int ci = 0; ci < nchunk; ++ci) {
             const bool more = ci + 1 < nchunk, update = more || has_out, with_x = OUT && (ci > 0 || has_in);
@@ -365,15 +373,15 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 }
                 __syncwarp();
             }
-            if (!wait_warp(S.kt, ci) || !wait_warp(S.fv, ci)) break;
+            if (!wait_warp(S.kt, ci) || !wait_warp(S.fv[ci % NV], ci / NV)) break;
             tc::fence_after();
             if (update) {                               // U = v^T K~
                 issued = true;
                 if (tc::elect_one()) {
-                    const uint64_t da = tc::sw128_desc(sv, D == 64 ? 0 : SUBB);
+                    const uint64_t da = tc::sw128_desc(sv(ci), D == 64 ? 0 : SUBB);
 #pragma unroll
                     for (int piece = 0; piece < PIECES; ++piece) {
-                        const uint64_t db = tc::sw128_desc(piece == 0 ? skh : piece == 1 ? skm : sk, SUBB);
+                        const uint64_t db = tc::sw128_desc(piece == 0 ? skh : piece == 1 ? skm : s3, SUBB);
 #pragma unroll
                         for (int k = 0; k < C / 16; ++k)
                             tc::mma_ss(tmem + kColU, da + 128 * k, db + 128 * k, kIdU, piece + k > 0);
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 if (OUT && !wait_warp(S.a, ci)) break;
                 if (tc::elect_one()) {
                     load_q(ci + 1);
-                    if (PIECES < 3) load_k(ci + 1);
+                    if (PIECES < 3 || !OUT) load_k(ci + 1);
                 }
                 ++loads_a;
                 __syncwarp();
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 if (!wait_warp(S.pr, ci)) break;
                 tc::fence_after();
                 if (tc::elect_one()) {
-                    const uint64_t db = tc::sw128_desc(sv, SUBB);
+                    const uint64_t db = tc::sw128_desc(sv(ci), SUBB);
                     const uint32_t acc = with_x ? 1u : 0u;
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
@@ -409,19 +417,25 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
             }
             if (!more) break;
             if ((OUT && !wait_warp(S.o, ci)) || !wait_warp(S.u, ci)) break;
-            if (tc::elect_one()) {
-                if (PIECES == 3) load_k(ci + 1);
-                load_v(ci + 1);
+            if (ci + NV < nchunk) {
+                if (tc::elect_one()) {
+                    if (PIECES == 3 && OUT) load_k(ci + 1);
+                    load_v(ci + NV);
+                }
+                ++loads_v;
+                __syncwarp();
             }
-            ++loads_v;
-            __syncwarp();
         }
         if (*abort) {
             // what was begun ends before the CTA's memory is given back
             const unsigned long long s0 = tc::global_ns();
-            while (nchunk > 0 && !(tc::mbar_test(&S.fa, (unsigned)(loads_a - 1) & 1u) &&
-                                   tc::mbar_test(&S.fv, (unsigned)(loads_v - 1) & 1u)) &&
-                   tc::global_ns() - s0 <= P.wait_ns) {
+            auto landed = [&]() {
+                bool all = tc::mbar_test(&S.fa, (unsigned)(loads_a - 1) & 1u);
+                for (int i = max(0, min(loads_v, nchunk) - NV); i < min(loads_v, nchunk); ++i)
+                    all = all && tc::mbar_test(&S.fv[i % NV], (unsigned)(i / NV) & 1u);
+                return all;
+            };
+            while (nchunk > 0 && !landed() && tc::global_ns() - s0 <= P.wait_ns) {
             }
             __syncwarp();
             if (issued) {
@@ -441,9 +455,9 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         const bool more = ci + 1 < nchunk, update = more || has_out, with_x = OUT && (ci > 0 || has_in);
         if (!wait_warp(S.fa, ci)) break;
         if (m < C) {  // rows of v past the chunk's tokens meet zeros of P and K~: 0 * NaN is NaN
-            if (!wait_warp(S.fv, ci)) break;
+            if (!wait_warp(S.fv[ci % NV], ci / NV)) break;
             for (int x = tid; x < (C - m) * 8 * SUB; x += kWork)
-                *reinterpret_cast<uint4*>(S.v + (x / ((C - m) * 8)) * SUBB + (m + x % ((C - m) * 8) / 8) * 128 +
+                *reinterpret_cast<uint4*>(S.v[ci % NV] + (x / ((C - m) * 8)) * SUBB + (m + x % ((C - m) * 8) / 8) * 128 +
                                           (x % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         if (update) {
@@ -477,7 +491,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                 }
                 *reinterpret_cast<uint4*>(S.kh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 if (PIECES >= 2) *reinterpret_cast<uint4*>(S.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-                if (PIECES == 3) *reinterpret_cast<uint4*>(S.k + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (PIECES == 3) *reinterpret_cast<uint4*>(third + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
         tc::fence_async_smem();
@@ -485,17 +499,10 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
         if (OUT) {
             if (!wait_warp(S.a, ci)) break;
             tc::fence_after();
-            // P: this warpgroup's blocks of the quarter's rows, d4 blocks back in (walked) time
-#pragma unroll
-            for (int jj = 0; jj < 4 / NWG; ++jj) {
-                const int d4 = NWG == 4 ? wg : (wg == 0 ? 3 * jj : 1 + jj);
-                const int j = rev ? (quad + d4) & 3 : (quad - d4) & 3;
-                if (d4 > wq || 32 * j >= m) {           // before the sequence's start, or past the chunk's end
-                    tc::tmem_zero<16 * PP>(lanes + 32 * j);
-                    continue;
-                }
-                p_block<PP>(lanes + 32 * j, j, d4, fast, rev, lane, m, S.pw, S.col, S.row);
-            }
+            // P: the quarter's rows, the block wg blocks back in (walked) time
+            const int j = rev ? (quad + wg) & 3 : (quad - wg) & 3;
+            if (wg > wq || 32 * j >= m) tc::tmem_zero<16 * PP>(lanes + 32 * j);  // before the sequence's start, or past the chunk's end
+            else p_block<PP>(lanes + 32 * j, j, wg, fast, rev, lane, m, S.pw, S.col, S.row);
             if (!fast && with_x) {
                 const int row = quad * 32 + lane;
                 const float2 f = f2(S.pw[max(rev ? m - 1 - row : row, 0) + e0] * pr.scale_inter);

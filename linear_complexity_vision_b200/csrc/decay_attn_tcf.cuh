@@ -119,15 +119,6 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     // chunk ci of the walk: its first token in the segment
     auto first = [&](int ci) { return (rev ? nchunk - 1 - ci : ci) * C; };
 
-    // X: row jr of X^T (a v channel), columns c0 .. (k channels); U has its rows twice
-    constexpr int NX = D * D / kWork;
-    const int jr = (quad & 1) * 32 + lane, c0 = ((quad >> 1) * 4 + wg) * NX;
-    float X[NX];
-#pragma unroll
-    for (int i = 0; i < NX; ++i)
-        X[i] = has_in && !issuer
-                   ? __ldg(pr.x_in + xo + (pr.x_in_t ? (size_t)jr * D + c0 + i : (size_t)(c0 + i) * D + jr)) : 0.f;
-
     // two 16-byte vectors (8 channels) of a tile a thread: rows vr, vr + 64, channels 8 vc ..
     const int vr = tid / 8, vc = tid % 8;
     const uint32_t voff = vr * 128 + ((vc ^ (vr & 7)) << 4);  // the second is 64 rows on: the same swizzle
@@ -156,6 +147,17 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(source(which, a + vr + 64 * i)));
             }
     };
+    if (!issuer && nchunk > 0) prefetch(0);
+
+    // X: row jr of X^T (a v channel), columns c0 .. (k channels); U has its rows twice
+    constexpr int NX = D * D / kWork;
+    const int jr = (quad & 1) * 32 + lane, c0 = ((quad >> 1) * 4 + wg) * NX;
+    float X[NX];
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+        X[i] = has_in && !issuer
+                   ? __ldg(pr.x_in + xo + (pr.x_in_t ? (size_t)jr * D + c0 + i : (size_t)(c0 + i) * D + jr)) : 0.f;
+
     // 8 values times f as the three pieces' vectors at off
     auto put = [&](uint8_t* p0, uint8_t* p1, uint8_t* p2, uint32_t off, const float* x, float f) {
         uint32_t w0[4], w1[4], w2[4];
