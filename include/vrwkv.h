@@ -469,10 +469,24 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  *            need no preparation.  Calls that may run at the same time need
  *            separate workspaces.
  * Limits: D <= 128 (UNSUPPORTED above).
- * Arithmetic: products, sums and states in float32; outputs rounded once.
+ * Arithmetic: sums, decays and states in float32, products on the tensor
+ *   cores from operands split into parts; outputs rounded once.
+ *   float32    what the parts leave out is below 2^-21 of a product.
+ *   bfloat16   q, k, v (gy) as they are; a state that meets q in two bfloat16
+ *              parts (2^-17), one that leaves the call formed from three
+ *              (2^-24).  The decayed products q.k and the decayed keys that
+ *              meet v are in two parts too; calls of B*T*H >= 8192 may round
+ *              them to one bfloat16: in outputs these roundings, half a step each
+ *              and independent, weigh as much as the final one.
+ *   Heads of a multiple of 8 channels (float32: 36 to 64, a multiple of 4) in
+ *   tensors whose rows, outputs and states are 16-byte aligned take the
+ *   fifth-generation tensor cores from 17 to 97 tokens on (by type and D), the
+ *   rest a kernel for any size.  On the former, where |w| <= 1/2, sums carry
+ *   factors within e^+-32: safe for outputs of magnitudes from 1e-24 to 1e24.
+ *   The same call on the same alignments gives the same bits; a sequence's
+ *   bits may differ between batches of other sizes.
  *   Infinities and NaN among the valid tokens may also reach outputs of
- *   earlier tokens of the same 128-token block.  The same call gives the same
- *   bits.
+ *   earlier tokens of the same 128-token block, as NaN.
  */
 
 size_t vrwkv_decay_attn_workspace_bytes(int B, int T, int H, int D,

@@ -72,12 +72,12 @@ int padded_d(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 // measured alone on an SM, in us for a unit of 128 tokens (and how much of
 // that each further CTA on the same SM adds):
 //                         outputs          states only      CTAs of an SM
-//   tensor cores, D = 64  1.75             2.0 (+ 0.5)      1 (persistent), 2
-//   tensor cores, D = 128 4.2              3.0              1
+//   tcgen05, D <= 64      1.75             2.0 (+ 0.5)      1 (persistent), 2
+//            D <= 128     4.2              3.0              1
+//            float32      7.3              4.5              1
 //   any size, DP = 32     9 (+ 0.6)        4 (+ 0.6)        3
 //             DP = 64     23 (+ 0.6)       9 (+ 0.6)        3
 //             DP = 128    45               18               1
-//   float32, D = 64       7.3              4.5              1
 // Both sides measured: B = 1, T = 4096, 16 heads of 64, bfloat16: one segment
 // 56 us, eight 32 us; B = 8: one segment 62 us, two 130 us.
 struct Cut {
@@ -103,7 +103,7 @@ double pass_us(long long ctas, int units, const PassCost& c) {
 Cut plan(int B, int T, int H, int D, vrwkv_dtype dtype, int nprob, bool tc) {
     static const PassCost kOut[6] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}, {7.3, 0, 1}};
     static const PassCost kState[6] = {{2.0, 0.5, 2}, {3.0, 0, 1}, {4, 0.6, 3}, {9, 0.6, 3}, {18, 0, 1}, {4.5, 0, 1}};
-    const int kind = tc ? (dtype == VRWKV_F32 ? 5 : D == 64 ? 0 : 1) : (D <= 32 ? 2 : D <= 64 ? 3 : 4);
+    const int kind = tc ? (dtype == VRWKV_F32 ? 5 : D <= 64 ? 0 : 1) : (D <= 32 ? 2 : D <= 64 ? 3 : 4);
     const int units = (T + kSegUnit - 1) / kSegUnit;
     const long long heads = (long long)B * H;
     Cut best = cut_into(T, 1);
@@ -124,9 +124,25 @@ Cut plan(int B, int T, int H, int D, vrwkv_dtype dtype, int nprob, bool tc) {
     return best;
 }
 
-// The tcgen05 kernels take heads of 64 channels and bfloat16 heads of 128;
+// The tcgen05 kernels take heads of whole 16-byte vectors, bfloat16 ones of up
+// to 128 channels, float32 ones of 33 to 64, and work on 128 tokens however few
+// there are; the kernel for any size works on 32.  Both measured, us, forward
+// (tcgen05 : any size), for 8, 160 and 1024 heads:
+//   bfloat16, D = 64   T = 16  5.6 : 5.6    7.5 : 6.0    16.7 : 15.8
+//                      T = 32  5.7 : 6.8    7.5 : 7.3    16.6 : 20.5
+//                      T = 128 6.0 : 25     7.3 : 28     16.9 : 88
+//             D = 32   T = 32  5.6 : 4.2    7.4 : 4.5    16.6 : 11.7
+//                      T = 64  5.8 : 6.8    6.9 : 7.6    16.6 : 21.7
+//             D = 128  T = 8   5.8 : 6.1    10.4 : 10.6  31.8 : 36.8
+//   float32,  D = 64   T = 64  10.3 : 11.5  19.7 : 13.5  71.6 : 42.8
+//                      T = 96  10.8 : 17.1  20.9 : 20.6  77.3 : 68.8
+//                      T = 128 11.3 : 22.7  21.6 : 27.6  79.8 : 94.2
+//             D = 32   T = 128 10.7 : 10.4  20.3 : 12.7  72.8 : 40.2
 // VRWKV_DECAY_TC=0 keeps them on the kernel for any size (diagnostics and tests).
-bool tc_sizes(int D, vrwkv_dtype dtype) { return D == 64 || (dtype == VRWKV_BF16 && D == 128); }
+bool tc_sizes(int T, int D, vrwkv_dtype dtype) {
+    if (dtype == VRWKV_F32) return D % 4 == 0 && D > 32 && D <= 64 && T > 96;
+    return D % 8 == 0 && T > (D <= 32 ? 32 : 16);
+}
 bool tc_disabled() {
     const char* e = getenv("VRWKV_DECAY_TC");
     return e && e[0] == '0' && e[1] == 0;
@@ -138,7 +154,7 @@ size_t state_floats(int B, int H, int D, int nseg) { return (size_t)B * H * nseg
 // depends on the tensors' alignment.
 size_t ws_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
     size_t need = 0;
-    for (int tc = 0; tc <= (tc_sizes(D, dtype) ? 1 : 0); ++tc) {
+    for (int tc = 0; tc <= (tc_sizes(T, D, dtype) ? 1 : 0); ++tc) {
         const Cut c = plan(B, T, H, D, dtype, backward ? 3 : 1, tc != 0);
         if (c.nseg > 1)
             need = std::max(need, ((backward ? 2 : 1) * state_floats(B, H, D, c.nseg) * 4 + 255) / 256 * 256);
@@ -169,28 +185,33 @@ vrwkv_status launch_io(const decay::Params& p, cudaStream_t s) {
 }
 
 // ---- tensor cores ----
-// A token tensor as TMA reads it: (C, T, B) with rows ld elements apart, in
-// boxes of 64 channels x 128 tokens (rows past T arrive as zeros).
-bool encode_tokens(CUtensorMap* m, const void* x, long long ld, int B, int T, int C) {
+// A token tensor as TMA reads it: (D, H, T, B) with rows ld elements apart, in
+// boxes of 64 channels of a head x 128 tokens (channels past D and rows past T
+// arrive as zeros and are not stored).
+bool encode_tokens(CUtensorMap* m, const void* x, long long ld, int B, int T, int H, int D) {
     const EncodeTiledFn enc = encode_fn();
-    const cuuint64_t dims[3] = {(cuuint64_t)C, (cuuint64_t)T, (cuuint64_t)B};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)T * ld * 2};
-    const cuuint32_t box[3] = {64, decay::kTcChunk, 1}, estr[3] = {1, 1, 1};
-    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr,
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2, (cuuint64_t)T * ld * 2};
+    const cuuint32_t box[4] = {64, 1, decay::kTcChunk, 1}, estr[4] = {1, 1, 1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(x), dims, strides, box, estr,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // Rows that start on 16-byte boundaries (and a stride that TMA can hold).
 bool rows16(const void* x, long long ld, int es) { return aligned(x, 16) && ld * es % 16 == 0 && ld < (1LL << 36); }
 
-template <int D, bool OUT, int PIECES, int PP>
-vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
+template <int D, bool OUT, int PIECES, int PP, bool PAD>
+vrwkv_status launch_tc_pad(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
     static std::atomic<int> granted{0};
     constexpr int smem = decay::tc_smem_bytes<D, OUT>();
-    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT, PIECES, PP>, granted, smem);
+    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT, PIECES, PP, PAD>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    decay::decay_attn_tc_kernel<D, OUT, PIECES, PP><<<ctas, decay::tc_threads<D>(), smem, s>>>(p);
+    decay::decay_attn_tc_kernel<D, OUT, PIECES, PP, PAD><<<ctas, decay::tc_threads<D>(), smem, s>>>(p);
     return cuda_status(cudaGetLastError(), "decay_attn_tc_kernel launch");
+}
+template <int D, bool OUT, int PIECES, int PP>
+vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
+    return OUT && p.p.D == D ? launch_tc_pad<D, OUT, PIECES, PP, !OUT>(p, ctas, s) : launch_tc_pad<D, OUT, PIECES, PP, true>(p, ctas, s);
 }
 template <int PIECES, int PP>
 vrwkv_status launch_tc64(decay::TcParams& p, cudaStream_t s) {
@@ -229,7 +250,7 @@ constexpr long long kRoundedRows = 8192;
 vrwkv_status launch_tc_any(decay::TcParams& p, bool exact, cudaStream_t s) {
     const unsigned n = (unsigned)p.nitems;
     const bool rounded = (long long)p.p.B * p.p.T * p.p.H >= kRoundedRows;
-    if (p.p.pr[0].out && p.p.D == 64) {
+    if (p.p.pr[0].out && p.p.D <= 64) {
         if (rounded) return exact ? launch_tc64<3, 1>(p, s) : launch_tc64<1, 1>(p, s);
         return exact ? launch_tc64<3, 2>(p, s) : launch_tc64<2, 2>(p, s);
     }
@@ -237,7 +258,7 @@ vrwkv_status launch_tc_any(decay::TcParams& p, bool exact, cudaStream_t s) {
         if (rounded) return exact ? launch_tc<128, true, 3, 1>(p, n, s) : launch_tc<128, true, 1, 1>(p, n, s);
         return exact ? launch_tc<128, true, 3, 2>(p, n, s) : launch_tc<128, true, 2, 2>(p, n, s);
     }
-    if (p.p.D == 64) return exact ? launch_tc<64, false, 3, 2>(p, n, s) : launch_tc<64, false, 2, 2>(p, n, s);
+    if (p.p.D <= 64) return exact ? launch_tc<64, false, 3, 2>(p, n, s) : launch_tc<64, false, 2, 2>(p, n, s);
     return exact ? launch_tc<128, false, 3, 2>(p, n, s) : launch_tc<128, false, 2, 2>(p, n, s);
 }
 
@@ -252,7 +273,7 @@ struct Launcher {
 
     const char* kernel(int D) const {
         return !tc ? "decay_attn_kernel" : dtype == VRWKV_F32 ? "decay_attn_tcf_kernel"
-                   : D == 64 ? "decay_attn_tc64_kernel" : "decay_attn_tc_kernel";
+                   : D <= 64 ? "decay_attn_tc64_kernel" : "decay_attn_tc_kernel";
     }
     int map_of(const char* x, long long row) const {
         for (int i = 0; i < 4; ++i)
@@ -275,20 +296,20 @@ struct Launcher {
     }
 };
 
-// The tensor-core kernel where the sizes, alignments and row strides of all
-// n <= 4 tensors allow, else the FP32 pipes.
+// The tcgen05 kernel where the sizes, alignments and row strides of all
+// n <= 4 tensors and of the states read allow, else the kernel for any size.
 Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long* ld, int n, const void* const* outs,
-                       int no, bool state_leaves, int B, int T, int H, int D) {
+                       int no, const float* state, const float* gstate, bool state_leaves, int B, int T, int H, int D) {
     Launcher l = {};
     l.dtype = dtype;
     l.exact = state_leaves;
-    l.tc = tc_sizes(D, dtype) && !tc_disabled();
-    l.t.wide_out = 1;
+    l.tc = tc_sizes(T, D, dtype) && !tc_disabled() && aligned(state, 16) && aligned(gstate, 16);
+    const int es = elem_bytes(dtype);
+    l.t.wide_out = D * es % 32 == 0;
     for (int i = 0; i < no; ++i) {
         l.tc = l.tc && aligned(outs[i], 16);
         if (!aligned(outs[i], 32)) l.t.wide_out = 0;
     }
-    const int es = elem_bytes(dtype);
     for (int i = 0; i < n && l.tc; ++i) l.tc = rows16(x[i], ld[i], es);
     if (!l.tc) return l;
     l.t.err = device_error_word();
@@ -298,10 +319,10 @@ Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long*
     for (int i = 0; i < n && l.tc; ++i) {
         l.src[i] = x[i];
         l.ld[i] = ld[i];
-        l.tc = encode_tokens(&l.t.map[i], x[i], ld[i], B, T, H * D);
+        l.tc = encode_tokens(&l.t.map[i], x[i], ld[i], B, T, H, D);
     }
-    for (int i = 0; i < no && l.tc && D == 64; ++i)
-        l.tc = encode_tokens(&l.t.omap[i], outs[i], H * D, B, T, H * D);
+    for (int i = 0; i < no && l.tc && D <= 64; ++i)
+        l.tc = encode_tokens(&l.t.omap[i], outs[i], (long long)H * D, B, T, H, D);
     return l;
 }
 
@@ -353,7 +374,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     const void* dsts[1] = {out};
     const long long lds[3] = {ldq, ldk, ldv};
     Launcher attn =
-        make_launcher(dtype, srcs, lds, 3, dsts, 1, state_out != nullptr, B, T, H, D);
+        make_launcher(dtype, srcs, lds, 3, dsts, 1, state, nullptr, state_out != nullptr, B, T, H, D);
     const Cut cut = plan(B, T, H, D, dtype, 1, attn.tc);
     decay::Params p = {};
     p.w = w;
@@ -440,7 +461,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     const void* dsts[3] = {gq, gk, gv};
     const long long lds[4] = {ldq, ldk, ldv, ldg};
     Launcher attn =
-        make_launcher(dtype, srcs, lds, 4, dsts, 3, gstate_in != nullptr, B, T, H, D);
+        make_launcher(dtype, srcs, lds, 4, dsts, 3, state, gstate, gstate_in != nullptr, B, T, H, D);
     const Cut cut = plan(B, T, H, D, dtype, 3, attn.tc);
     decay::Params p = {};
     p.w = w;

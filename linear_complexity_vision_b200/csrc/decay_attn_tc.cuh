@@ -1,6 +1,7 @@
 // Multi-head decay attention on the 5th-generation tensor cores: the operator
 // of decay_attn.cuh (the same problems, segments and states) for bfloat16 and
-// heads of D = 128 (states: also 64) channels, in chunks of 128 tokens.
+// heads of up to D = 128 (states: also 64) channels, in chunks of 128 tokens.
+// Narrower heads, of whole 16-byte vectors, are zero-padded to D by TMA.
 //
 // Per chunk, with q, k, v tiles brought by TMA (128-byte swizzle) and X^T, the
 // state, in float32 registers:
@@ -56,11 +57,11 @@ constexpr float kTcFastW = 0.5f;
 constexpr unsigned kTcErr = 8u;
 
 struct TcParams {
-    CUtensorMap map[4];      // (C, T, B) tensors: box (64, 128, 1), 128-byte swizzle
+    CUtensorMap map[4];      // (D, H, T, B) tensors: box (64, 1, 128, 1), 128-byte swizzle, zeros past D and T
     CUtensorMap omap[3];     // the problems' outputs, likewise
     Params p;
     int mq[3], mk[3], mv[3]; // maps of the problems' q, k, v
-    int wide_out;            // outputs are 32-byte aligned
+    int wide_out;            // the outputs' rows of a head are 32-byte aligned
     int nitems;              // CTAs, or work items of the persistent kernel
     int step[4];             // its CTAs' stride in items, as (problem, segment, head, sequence)
     unsigned int* err;
@@ -184,13 +185,45 @@ __device__ __forceinline__ void p_block(uint32_t taddr, int j, int d4, bool fast
     }
 }
 
+// Row jr of X^T, columns c0 .. c0 + NX, from a (d, d) state, zeros past d (a
+// multiple of 4; the state 16-byte aligned).  No load waits for a branch.
+template <int NX>
+__device__ __forceinline__ void load_x(float (&X)[NX], const float* x, bool transposed, int jr, int c0, int d) {
+    const int here = jr < d ? d - c0 : 0;
+    if (transposed) {
+#pragma unroll
+        for (int i = 0; i < NX; i += 4) {
+            const float4 y = __ldg(reinterpret_cast<const float4*>(x + (i < here ? jr * d + c0 + i : 0)));
+            X[i] = i < here ? y.x : 0.f;
+            X[i + 1] = i < here ? y.y : 0.f;
+            X[i + 2] = i < here ? y.z : 0.f;
+            X[i + 3] = i < here ? y.w : 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const float y = __ldg(x + (i < here ? (c0 + i) * d + jr : 0));
+            X[i] = i < here ? y : 0.f;
+        }
+    }
+}
+template <int NX>
+__device__ __forceinline__ void store_x_out(const float (&X)[NX], float* x, bool transposed, int jr, int c0, int d) {
+    const int here = jr < d ? d - c0 : 0;
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+        if (i < here) x[transposed ? jr * d + c0 + i : (c0 + i) * d + jr] = X[i];
+}
+
 __device__ __forceinline__ void st_global_32(char* p, const uint32_t (&r)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
-template <int D, bool OUT, int PIECES, int PP>
+// PAD: heads may be narrower than D.  (With the width a variable in every
+// launch, B = 1, T = 16384, 8 heads of 128 took 87 us in place of 80.)
+template <int D, bool OUT, int PIECES, int PP, bool PAD>
 __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     decay_attn_tc_kernel(const __grid_constant__ TcParams P) {
     static_assert(D == 128 || !OUT, "outputs of D = 64 have a kernel of their own");
@@ -216,7 +249,8 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     const int rev = pr.reverse, e0 = rev ? 0 : 1;
     const int nchunk = (n + C - 1) / C;
     const bool has_in = pr.x_in != nullptr, has_out = pr.x_out != nullptr;
-    const size_t xo = ((size_t)bh * p.nseg + seg) * D * D;
+    const int d = PAD ? p.D : D;                        // channels there are; operands are zero past them
+    const size_t xo = ((size_t)bh * p.nseg + seg) * d * d;
 
     if (tid == 0) {
         tc::mbar_init(&S.fa, 1);
@@ -271,7 +305,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     auto load = [&](uint32_t dst, int map, int ci, unsigned long long* bar) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
-            tc::tma_load_3d(dst + s * SUBB, &P.map[map], h * D + 64 * s, t0 + first(ci), b, bar);
+            tc::tma_load_4d(dst + s * SUBB, &P.map[map], 64 * s, h, t0 + first(ci), b, bar);
     };
     __syncthreads();
     const bool issuer = warp == NW;
@@ -297,10 +331,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     const int c0 = D == 64 ? ((quad >> 1) * 2 + wg) * NX : wg * NX;
     float X[NX];
     if (has_in && !issuer) {
-        const float* x = pr.x_in + xo;
-#pragma unroll
-        for (int i = 0; i < NX; ++i)
-            X[i] = __ldg(pr.x_in_t ? x + (size_t)jr * D + c0 + i : x + (size_t)(c0 + i) * D + jr);
+        load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, d);
     } else {
 #pragma unroll
         for (int i = 0; i < NX; ++i) X[i] = 0.f;
@@ -550,31 +581,28 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
             arrive_warp(S.of);
             if (row < m) {
                 const float2 f = f2(fast ? S.row[row] : 1.0f);
-                char* dst = pr.out + ((((size_t)b * p.T + t0 + a + row) * p.H + h) * D + wg * 32) * 2;
+                char* dst = pr.out + ((((size_t)b * p.T + t0 + a + row) * p.H + h) * d + wg * 32) * 2;
+                const int here = d - wg * 32;           // channels there are
 #pragma unroll
                 for (int i = 0; i < 32; i += 16) {
                     uint32_t o[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] = pack_bf16(mul2(f2(v[i + 2 * e], v[i + 2 * e + 1]), f));
                     if (P.wide_out) {
-                        st_global_32(dst + 2 * i, o);
+                        if (i < here) st_global_32(dst + 2 * i, o);
                     } else {
-                        *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(dst + 2 * i + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+                        if (i < here) *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (i + 8 < here) *reinterpret_cast<uint4*>(dst + 2 * i + 16) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
                 }
             }
         }
     }
-    if (has_out && !issuer && ci == nchunk) {
-        float* x = pr.x_out + xo;
-#pragma unroll
-        for (int i = 0; i < NX; ++i) x[pr.x_out_t ? (size_t)jr * D + c0 + i : (size_t)(c0 + i) * D + jr] = X[i];
-    }
+    if (has_out && !issuer && ci == nchunk) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, d);
     if (OUT) {  // rows past the sequence's end
-        for (int x = tid; x < (t_end - n) * (D / 8); x += kThreads)
-            *reinterpret_cast<uint4*>(pr.out + (((size_t)b * p.T + t0 + n + x / (D / 8)) * p.H + h) * D * 2 +
-                                      (x % (D / 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        for (int x = tid; x < (t_end - n) * (d / 8); x += kThreads)
+            *reinterpret_cast<uint4*>(pr.out + (((size_t)b * p.T + t0 + n + x / (d / 8)) * p.H + h) * d * 2 +
+                                      (x % (d / 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
     tc::fence_before();
     __syncthreads();

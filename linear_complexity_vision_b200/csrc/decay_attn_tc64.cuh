@@ -1,6 +1,6 @@
 // Multi-head decay attention on the 5th-generation tensor cores for bfloat16
-// heads of 64 channels: the operator and the steps of a chunk are those of
-// decay_attn_tc.cuh.  Here a persistent CTA (one per SM) keeps two chunks at
+// heads of up to 64 channels (zero-padded to 64): the operator and the steps of
+// a chunk are those of decay_attn_tc.cuh.  Here a persistent CTA (one per SM) keeps two chunks at
 // work at a time, each on a stream of its own (tiles, tensor memory, 8 worker
 // warps, an issuing warp), and walks all its work items, one head's segment
 // after the other, without a break: the next item's tiles are loaded and its
@@ -86,7 +86,7 @@ struct T64Item {
         has_out = pr.x_out != nullptr;
     }
     __device__ __forceinline__ long long state_at(const Params& p) const {
-        return (((long long)b * p.H + h) * p.nseg + seg) * 64 * 64;
+        return (((long long)b * p.H + h) * p.nseg + seg) * p.D * p.D;
     }
     __device__ __forceinline__ bool fast() const { return fabsf(w) <= kTcFastW; }
 };
@@ -312,10 +312,11 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
             it.at(P, blockIdx.x);
             for (int item = blockIdx.x; item < nitems; item += gridDim.x, it.step(P)) {
                 const int r0 = it.nchunk * C, rows = min(p.seg_tokens, p.T - it.t0) - r0;
-                for (int x = tid; x < rows * 8; x += 512)
+                const int vecs = p.D / 8;
+                for (int x = tid; x < rows * vecs; x += 512)
                     *reinterpret_cast<uint4*>(p.pr[it.prob].out +
-                                              (((size_t)it.b * p.T + it.t0 + r0 + x / 8) * p.H + it.h) * D * 2 +
-                                              (x % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                              (((size_t)it.b * p.T + it.t0 + r0 + x / vecs) * p.H + it.h) * p.D * 2 +
+                                              (x % vecs) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
         }
     } else if (warp < 20) {
@@ -335,20 +336,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
             const long long xo = it.state_at(p);
             float X[NX];
             if (it.has_in) {
-                const float* x = pr.x_in + xo;
-                if (pr.x_in_t) {
-#pragma unroll
-                    for (int i = 0; i < NX; i += 4) {
-                        const float4 y = __ldg(reinterpret_cast<const float4*>(x + jr * D + c0 + i));
-                        X[i] = y.x;
-                        X[i + 1] = y.y;
-                        X[i + 2] = y.z;
-                        X[i + 3] = y.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NX; ++i) X[i] = __ldg(x + (c0 + i) * D + jr);
-                }
+                load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, p.D);
             } else {
 #pragma unroll
                 for (int i = 0; i < NX; ++i) X[i] = 0.f;
@@ -412,11 +400,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 if (more) okay = next_x(tokens(ci + 1), s ^ 1);
                 if (!okay) break;
             }
-            if (it.has_out && okay) {
-                float* x = pr.x_out + xo;
-#pragma unroll
-                for (int i = 0; i < NX; ++i) x[pr.x_out_t ? jr * D + c0 + i : (c0 + i) * D + jr] = X[i];
-            }
+            if (it.has_out && okay) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, p.D);
         }
     } else {
         // ---- issuer of a stream ----
@@ -432,7 +416,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         const uint32_t skh = tc::smem_u32(T.kh), skm = tc::smem_u32(T.km);
         const uint32_t sxh = PIECES == 1 ? skm : tc::smem_u32(S.x), sxl = sxh + 8192, sout = tc::smem_u32(T.out);
         auto load = [&](uint32_t dst, int map, const T64Cursor& c, unsigned long long* bar) {
-            tc::tma_load_3d(dst, &P.map[map], c.it.h * D, c.it.t0 + c.first(), c.it.b, bar);
+            tc::tma_load_4d(dst, &P.map[map], 0, c.it.h, c.it.t0 + c.first(), c.it.b, bar);
         };
         auto load_q = [&](const T64Cursor& c) {         // begins fa's phase; k completes it
             tc::mbar_expect_tx(&B.fa, 2 * 16384);
@@ -457,11 +441,11 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
             loads_a = loads_v = 1;
         }
         // the finished chunk's output tile; the lane that begins stores also waits for them
-        int out_map = 0, out_c = 0, out_t = 0, out_b = 0, out_ph = -1;
+        int out_map = 0, out_h = 0, out_t = 0, out_b = 0, out_ph = -1;
         auto store_out = [&]() {
             if (out_ph < 0) return true;
             if (!wait(B.so, out_ph)) return false;
-            if (tc::elect_one()) tc::tma_store_3d(&P.omap[out_map], sout, out_c, out_t, out_b);
+            if (tc::elect_one()) tc::tma_store_4d(&P.omap[out_map], sout, 0, out_h, out_t, out_b);
             __syncwarp();
             out_ph = -1;
             return true;
@@ -571,7 +555,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 __syncwarp();
             }
             out_map = cu.it.prob;
-            out_c = cu.it.h * D;
+            out_h = cu.it.h;
             out_t = cu.it.t0 + cu.first();
             out_b = cu.it.b;
             out_ph = ph;

@@ -1,6 +1,6 @@
 // Multi-head decay attention on the 5th-generation tensor cores for float32
-// heads of 64 channels: the operator of decay_attn.cuh (the same problems,
-// segments and states) in chunks of 128 tokens, as in decay_attn_tc.cuh.
+// heads of up to 64 channels, whole 16-byte vectors, zero-padded to 64: the
+// operator of decay_attn.cuh (the same problems, segments and states) in chunks of 128 tokens, as in decay_attn_tc.cuh.
 //
 // A float32 value is exactly the sum of three bfloat16 pieces h + m + l, each
 // the rounded remainder of the last.  A product is taken as the six products
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     const int rev = pr.reverse, e0 = rev ? 0 : 1;
     const int nchunk = (n + C - 1) / C;
     const bool has_in = pr.x_in != nullptr, has_out = pr.x_out != nullptr;
-    const size_t xo = ((size_t)bh * p.nseg + seg) * D * D;
+    const int d = p.D;                           // channels there are; operands are zero past them
+    const size_t xo = ((size_t)bh * p.nseg + seg) * d * d;
 
     if (tid == 0) {
         tc::mbar_init(&S.kt, NW);
@@ -126,22 +127,22 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     auto source = [&](int which, int token) {
         const char* x = which == 0 ? pr.q : which == 1 ? pr.k : pr.v;
         const long long ld = which == 0 ? pr.ldq : which == 1 ? pr.ldk : pr.ldv;
-        return reinterpret_cast<const float4*>(x + ((row0 + token) * (size_t)ld + h * D + 8 * vc) * 4);
+        return reinterpret_cast<const float4*>(x + ((row0 + token) * (size_t)ld + h * d + 8 * vc) * 4);
     };
-    auto fetch = [&](int which, int i, int a, int m, float (&d)[8]) {
+    auto fetch = [&](int which, int i, int a, int m, float (&x)[8]) {
         float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
         if (vr + 64 * i < m) {
             const float4* src = source(which, a + vr + 64 * i);
-            lo = __ldg(src);
-            hi = __ldg(src + 1);
+            if (8 * vc < d) lo = __ldg(src);
+            if (8 * vc + 4 < d) hi = __ldg(src + 1);
         }
-        d[0] = lo.x, d[1] = lo.y, d[2] = lo.z, d[3] = lo.w, d[4] = hi.x, d[5] = hi.y, d[6] = hi.z, d[7] = hi.w;
+        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
     };
     auto prefetch = [&](int ci) {
         const int a = first(ci), m = min(C, n - a);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (vr + 64 * i < m) {
+            if (vr + 64 * i < m && 8 * vc < d) {
 #pragma unroll
                 for (int which = OUT ? 0 : 1; which < 3; ++which)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(source(which, a + vr + 64 * i)));
@@ -153,10 +154,12 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     constexpr int NX = D * D / kWork;
     const int jr = (quad & 1) * 32 + lane, c0 = ((quad >> 1) * 4 + wg) * NX;
     float X[NX];
+    if (has_in && !issuer) {
+        load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, d);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NX; ++i)
-        X[i] = has_in && !issuer
-                   ? __ldg(pr.x_in + xo + (pr.x_in_t ? (size_t)jr * D + c0 + i : (size_t)(c0 + i) * D + jr)) : 0.f;
+        for (int i = 0; i < NX; ++i) X[i] = 0.f;
+    }
 
     // 8 values times f as the three pieces' vectors at off
     auto put = [&](uint8_t* p0, uint8_t* p1, uint8_t* p2, uint32_t off, const float* x, float f) {
@@ -357,8 +360,8 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
                 if (!fast) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const int c = 32 * j + i, d = rev ? c - row : row - c;
-                        v[i] *= S.pw[max(d, 0)] * pr.scale_intra;
+                        const int c = 32 * j + i;
+                        v[i] *= S.pw[max(rev ? c - row : row - c, 0)] * pr.scale_intra;
                     }
                 }
                 if (wg == 0) {                          // the diagonal block: columns in the row's future
@@ -435,7 +438,8 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
             tc::fence_after();
             const int row = quad * 32 + lane;
             const float f = fast ? S.row[row] : 1.0f;
-            char* dst = pr.out + ((((size_t)b * p.T + t0 + a + row) * p.H + h) * D + wg * 16) * 4;
+            char* dst = pr.out + ((((size_t)b * p.T + t0 + a + row) * p.H + h) * d + wg * 16) * 4;
+            const int here = d - wg * 16;               // channels there are
 #pragma unroll
             for (int i = 0; i < 16; i += 8) {
                 float y[8], s[8];
@@ -446,24 +450,20 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
                 for (int e = 0; e < 8; ++e) o[e] = __float_as_uint((y[e] + s[e]) * f);
                 if (row >= m) continue;
                 if (P.wide_out) {
-                    st_global_32(dst + 4 * i, o);
+                    if (i < here) st_global_32(dst + 4 * i, o);
                 } else {
-                    *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(dst + 4 * i + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+                    if (i < here) *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (i + 4 < here) *reinterpret_cast<uint4*>(dst + 4 * i + 16) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
             }
             tc::fence_before();
             arrive(S.of);
         }
     }
-    if (has_out && !issuer && ci == nchunk) {
-        float* x = pr.x_out + xo;
-#pragma unroll
-        for (int i = 0; i < NX; ++i) x[pr.x_out_t ? (size_t)jr * D + c0 + i : (size_t)(c0 + i) * D + jr] = X[i];
-    }
+    if (has_out && !issuer && ci == nchunk) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, d);
     if (OUT) {  // rows past the sequence's end
-        for (int x = tid; x < (t_end - n) * (D / 4); x += kTfThreads)
-            *reinterpret_cast<uint4*>(pr.out + ((((size_t)b * p.T + t0 + n + x / (D / 4)) * p.H + h) * D + (x % (D / 4)) * 4) * 4) =
+        for (int x = tid; x < (t_end - n) * (d / 4); x += kTfThreads)
+            *reinterpret_cast<uint4*>(pr.out + ((((size_t)b * p.T + t0 + n + x / (d / 4)) * p.H + h) * d + (x % (d / 4)) * 4) * 4) =
                 make_uint4(0u, 0u, 0u, 0u);
     }
     tc::fence_before();

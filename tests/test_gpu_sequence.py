@@ -77,7 +77,10 @@ def _ops(D, T):
     return 2 * (2 * D + 128 + T) + 16 + 104
 
 
-TC_SIZES = (64, 128)
+def _on_tcgen05(dt, T, D):
+    """Heads of whole 16-byte vectors, bfloat16 ones up to 128 channels, float32
+    ones of 33 to 64, of enough tokens."""
+    return D % 8 == 0 and T > (32 if D <= 32 else 16) if dt == "bf16" else D % 4 == 0 and 32 < D <= 64 and T > 96
 
 
 class Problem:
@@ -96,7 +99,7 @@ class Problem:
         self.w, self.wd = _dev(np.exp(r.uniform(-6, 0.5, H)) if w is None else np.full(H, w, float))
         self.s, self.sd = _dev(r.normal(size=(B, H, D, D)) if state else None)
         self.gs, self.gsd = _dev(r.normal(size=(B, H, D, D)) if state else None)
-        self.rounded = dt == "bf16" and D in TC_SIZES and B * T * H >= 8192
+        self.rounded = dt == "bf16" and _on_tcgen05(dt, T, D) and B * T * H >= 8192
         self.lens = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
         self.lensd = lens
 
@@ -151,12 +154,21 @@ CASES = [
     ("f32", 2, 100, 2, 100, False, False, None),
     ("f32", 1, 64, 3, 7, False, True, None),
     ("f32", 2, 32, 1, 32, True, True, [31, 32]),
+    ("bf16", 2, 150, 2, 8, True, True, [150, 20]),        # heads that are padded on their way in
+    ("bf16", 1, 1300, 3, 24, True, True, None),
+    ("bf16", 2, 200, 2, 72, True, True, [200, 90]),
+    ("bf16", 1, 1100, 2, 120, False, True, None),
+    ("f32", 2, 140, 3, 4, True, True, [140, 70]),
+    ("f32", 1, 1100, 2, 36, True, True, None),
+    ("f32", 3, 200, 1, 60, False, True, [200, 0, 131]),
+    ("f32", 1, 300, 2, 66, True, True, None),
 ]
 
 
-def _kernel(dt, D):
-    return {("bf16", 64): "decay_attn_tc64_kernel", ("bf16", 128): "decay_attn_tc_kernel",
-            ("f32", 64): "decay_attn_tcf_kernel"}.get((dt, D), "decay_attn_kernel")
+def _kernel(dt, T, D):
+    if not _on_tcgen05(dt, T, D):
+        return "decay_attn_kernel"
+    return "decay_attn_tcf_kernel" if dt == "f32" else "decay_attn_tc64_kernel" if D <= 64 else "decay_attn_tc_kernel"
 
 
 @pytest.mark.parametrize("dt,B,T,H,D,packed,state,lens", CASES)
@@ -164,7 +176,7 @@ def test_forward(vk, dt, B, T, H, D, packed, state, lens):
     p = Problem(dt, B, T, H, D, 1, packed, state, lens)
     out, last = p.fwd(vk)
     vk.device_status()
-    assert vk.load_library().vrwkv_last_kernel().decode() == _kernel(dt, D)
+    assert vk.load_library().vrwkv_last_kernel().decode() == _kernel(dt, T, D)
     p.check_fwd(out, last)
     again = p.fwd(vk)
     assert (again[0] == out).all() and (again[1] == last).all()
@@ -178,7 +190,7 @@ def test_backward(vk, dt, B, T, H, D, packed, state, lens):
     p = Problem(dt, B, T, H, D, 2, packed, state, lens)
     got = p.bwd(vk)
     vk.device_status()
-    assert vk.load_library().vrwkv_last_kernel().decode() == _kernel(dt, D)
+    assert vk.load_library().vrwkv_last_kernel().decode() == _kernel(dt, T, D)
     p.check_bwd(got)
     again = p.bwd(vk)
     for a, b in zip(got, again):
@@ -243,6 +255,68 @@ def test_heads_of_128(vk, B, T, H, lens):
     p.check_fwd(p.fwd(vk, want_state=False)[0], None)
     p.check_bwd(p.bwd(vk))
     vk.device_status()
+
+
+@pytest.mark.parametrize("dt,B,T,H,D", [("bf16", 30, 300, 3, 40), ("bf16", 2, 2100, 2, 16), ("bf16", 25, 200, 5, 96),
+                                        ("bf16", 1, 4200, 2, 88), ("f32", 40, 150, 4, 44), ("f32", 2, 1500, 2, 32)])
+def test_padded_heads_and_their_neighbours(vk, dt, B, T, H, D):
+    """Heads narrower than the tensor cores' tiles, several a CTA and cut: only
+    their own channels are written, inside buffers whose rest keeps its values."""
+    import torch
+    r = np.random.default_rng([20, D])
+    p = Problem(dt, B, T, H, D, 20, True, True, [int(x) for x in r.integers(0, T + 1, B - 1)] + [T],
+                w=np.exp(np.linspace(-4, 0.3, H)))
+    assert p.rounded == (dt == "bf16")
+    n, ns = B * T * H * D, p.s.numel()
+    buf, last = torch.full((n + 256,), 7.0, dtype=p.q.dtype, device="cuda"), torch.full((ns + 64,), 7.0, device="cuda")
+    got = p.fwd(vk, out=buf[128:128 + n].view(B, T, H * D), state_out=last[32:32 + ns].view(p.s.shape))
+    assert vk.load_library().vrwkv_last_kernel().decode() == _kernel(dt, T, D)
+    p.check_fwd(*got)
+    for b, m in ((buf, 128), (last, 32)):
+        assert (b[:m] == 7).all() and (b[-m:] == 7).all()
+    p.check_fwd(p.fwd(vk, want_state=False)[0], None)
+    p.check_bwd(p.bwd(vk))
+    vk.device_status()
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 20), ("bf16", 9)])
+@pytest.mark.parametrize("T", [100, 1500])
+def test_states_between_vector_boundaries(vk, dt, D, T):
+    """States and their gradients that start 4 bytes past a 16-byte boundary."""
+    import torch
+    p = Problem(dt, 1, T, 1, D, 21)
+    odd = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)  # noqa: E731
+    p.s, p.gs = odd(p.s), odd(p.gs)
+    assert p.s.data_ptr() % 16 == 4
+    p.check_fwd(*p.fwd(vk, state_out=odd(p.s)))
+    p.check_bwd(p.bwd(vk))
+
+
+def test_rows_and_states_far_apart(vk):
+    """Rows whose offsets pass 32 bits, in elements, and a pool of states of
+    more than 4 GiB."""
+    import torch
+    for dt, D in (("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 7)):
+        ld, T = (1 << 33) // 520 // 16 * 16, 530
+        p = Problem(dt, 1, T, 1, D, 22)
+        far = torch.empty(ld * T, dtype=p.q.dtype, device="cuda")
+        for i, name in enumerate("qkvg"):
+            t = far.as_strided((1, T, D), (ld * T, ld, 1), i * D)
+            t.copy_(getattr(p, name))
+            setattr(p, name, t)
+        p.check_fwd(*p.fwd(vk))
+        p.check_bwd(p.bwd(vk))
+        del far, t
+        p.q = p.k = p.v = p.g = None
+    N, D = 70000, 128
+    pool = torch.empty((N, 1, D, D), device="cuda")
+    slots = torch.tensor([N - 1, 0, 40000], dtype=torch.int32, device="cuda")
+    p = Problem("bf16", 3, 1, 1, D, 23)
+    pool[slots.long()] = p.s
+    q, k, v = (t[:, 0].contiguous() for t in (p.q, p.k, p.v))
+    out = vk.decay_attn_step(q, k, v, p.w, 1, pool, slots=slots, scale=p.scale)
+    vk.device_status()
+    p.check_fwd(out[:, None], pool[slots.long()])
 
 
 @pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 40)])
