@@ -254,24 +254,31 @@ __global__ void __launch_bounds__(1024) layer_norm_bwd_kernel(const LayerNormBwd
     }
 }
 
-// ggamma[c], gbeta[c]: the sums of n partial rows of 2C floats.  A CTA takes
-// 32 of the 2C columns; its 32 warps take every 32nd row.
+// ggamma[c], gbeta[c]: the sums of n partial rows of 2C floats.  A CTA takes 8
+// of the 2C columns (a 32-byte sector of each row), its 128 groups of 8 threads
+// every 128th row: the few hundred rows there are take one or two round trips
+// to L2.
+constexpr int kLnWgradCols = 8;
+
 __global__ void __launch_bounds__(1024) layer_norm_wgrad_kernel(const float* part, int n, int C, float* ggamma,
                                                                 float* gbeta) {
-    __shared__ float sm[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    __shared__ float sm[32][kLnWgradCols];
+    const int tid = threadIdx.x, col = tid % kLnWgradCols, group = tid / kLnWgradCols;
+    const int c = blockIdx.x * kLnWgradCols + col;
     float s = 0.f;
     if (c < 2 * C) {
 #pragma unroll 8
-        for (int i = warp; i < n; i += 32) s += part[(size_t)i * 2 * C + c];
+        for (int i = group; i < n; i += 1024 / kLnWgradCols) s += __ldg(part + (size_t)i * 2 * C + c);
     }
-    sm[warp][lane] = s;
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if ((tid & 31) < kLnWgradCols) sm[tid >> 5][col] = s;
     __syncthreads();
-    const float t = warp_sum(sm[lane][warp]);  // column warp of the CTA's 32
-    const int cw = blockIdx.x * 32 + warp;
-    if (lane == 0 && cw < C) ggamma[cw] = t;
-    else if (lane == 0 && cw < 2 * C) gbeta[cw - C] = t;
+    if (tid >= 32 * kLnWgradCols) return;
+    const int of = tid >> 5, cw = blockIdx.x * kLnWgradCols + of;
+    const float t = warp_sum(sm[tid & 31][of]);  // column of of the CTA's 8
+    if ((tid & 31) == 0 && cw < C) ggamma[cw] = t;
+    else if ((tid & 31) == 0 && cw < 2 * C) gbeta[cw - C] = t;
 }
 
 }  // namespace vrwkv
