@@ -84,6 +84,63 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     const int d = p.D;                           // channels there are; operands are zero past them
     const size_t xo = ((size_t)bh * p.nseg + seg) * d * d;
 
+    // chunk ci of the walk: its first token in the segment
+    auto first = [&](int ci) { return (rev ? nchunk - 1 - ci : ci) * C; };
+
+    // two 16-byte vectors (8 channels) of a tile a thread: rows vr, vr + 64, channels 8 vc ..
+    const int vr = tid / 8, vc = tid % 8;
+    const uint32_t voff = vr * 128 + ((vc ^ (vr & 7)) << 4);  // the second is 64 rows on: the same swizzle
+    const size_t row0 = (size_t)b * p.T + t0;
+    auto source = [&](int which, int token) {
+        const char* x = which == 0 ? pr.q : which == 1 ? pr.k : pr.v;
+        const long long ld = which == 0 ? pr.ldq : which == 1 ? pr.ldk : pr.ldv;
+        return reinterpret_cast<const float4*>(x + ((row0 + token) * (size_t)ld + h * d + 8 * vc) * 4);
+    };
+    auto fetch = [&](int which, int i, int a, int m, float (&x)[8]) {
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+        if (vr + 64 * i < m) {
+            const float4* src = source(which, a + vr + 64 * i);
+            if (8 * vc < d) lo = __ldg(src);
+            if (8 * vc + 4 < d) hi = __ldg(src + 1);
+        }
+        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+    };
+    auto prefetch = [&](int ci, int from) {             // q, k, v from the from-th on
+        const int a = first(ci), m = min(C, n - a);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (vr + 64 * i < m && 8 * vc < d) {
+#pragma unroll
+                for (int which = 0; which < 3; ++which)
+                    if (which >= from) asm volatile("prefetch.global.L2 [%0];" ::"l"(source(which, a + vr + 64 * i)));
+            }
+    };
+    // 8 values times f as the three pieces' vectors at off
+    auto put = [&](uint8_t* p0, uint8_t* p1, uint8_t* p2, uint32_t off, const float* x, float f) {
+        uint32_t w0[4], w1[4], w2[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float2 y = mul2(f2(x[2 * e], x[2 * e + 1]), f2(f));
+            w0[e] = split_bf16(y);
+            w1[e] = split_bf16(y);
+            w2[e] = pack_bf16(y);
+        }
+        *reinterpret_cast<uint4*>(p0 + off) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+        *reinterpret_cast<uint4*>(p1 + off) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        *reinterpret_cast<uint4*>(p2 + off) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+    };
+    // the first chunk's q and k are on their way before all else
+    float rq[2][8], rk[2][8];
+    if (!issuer && nchunk > 0) {
+        const int a = first(0), m = min(C, n - a);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (OUT) fetch(0, i, a, m, rq[i]);
+            fetch(1, i, a, m, rk[i]);
+        }
+        prefetch(0, 2);
+    }
+
     if (tid == 0) {
         tc::mbar_init(&S.kt, NW);
         tc::mbar_init(&S.kt2, NW);
@@ -117,38 +174,6 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bar);
     };
-    // chunk ci of the walk: its first token in the segment
-    auto first = [&](int ci) { return (rev ? nchunk - 1 - ci : ci) * C; };
-
-    // two 16-byte vectors (8 channels) of a tile a thread: rows vr, vr + 64, channels 8 vc ..
-    const int vr = tid / 8, vc = tid % 8;
-    const uint32_t voff = vr * 128 + ((vc ^ (vr & 7)) << 4);  // the second is 64 rows on: the same swizzle
-    const size_t row0 = (size_t)b * p.T + t0;
-    auto source = [&](int which, int token) {
-        const char* x = which == 0 ? pr.q : which == 1 ? pr.k : pr.v;
-        const long long ld = which == 0 ? pr.ldq : which == 1 ? pr.ldk : pr.ldv;
-        return reinterpret_cast<const float4*>(x + ((row0 + token) * (size_t)ld + h * d + 8 * vc) * 4);
-    };
-    auto fetch = [&](int which, int i, int a, int m, float (&x)[8]) {
-        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-        if (vr + 64 * i < m) {
-            const float4* src = source(which, a + vr + 64 * i);
-            if (8 * vc < d) lo = __ldg(src);
-            if (8 * vc + 4 < d) hi = __ldg(src + 1);
-        }
-        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
-    };
-    auto prefetch = [&](int ci) {
-        const int a = first(ci), m = min(C, n - a);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (vr + 64 * i < m && 8 * vc < d) {
-#pragma unroll
-                for (int which = OUT ? 0 : 1; which < 3; ++which)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(source(which, a + vr + 64 * i)));
-            }
-    };
-    if (!issuer && nchunk > 0) prefetch(0);
 
     // X: row jr of X^T (a v channel), columns c0 .. (k channels); U has its rows twice
     constexpr int NX = D * D / kWork;
@@ -161,20 +186,6 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
         for (int i = 0; i < NX; ++i) X[i] = 0.f;
     }
 
-    // 8 values times f as the three pieces' vectors at off
-    auto put = [&](uint8_t* p0, uint8_t* p1, uint8_t* p2, uint32_t off, const float* x, float f) {
-        uint32_t w0[4], w1[4], w2[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float2 y = mul2(f2(x[2 * e], x[2 * e + 1]), f2(f));
-            w0[e] = split_bf16(y);
-            w1[e] = split_bf16(y);
-            w2[e] = pack_bf16(y);
-        }
-        *reinterpret_cast<uint4*>(p0 + off) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-        *reinterpret_cast<uint4*>(p1 + off) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-        *reinterpret_cast<uint4*>(p2 + off) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-    };
     // factors of a whole chunk; a shorter one has its own
     const float x_full = fast ? decay_pow(base, 64) * pr.scale_inter : 1.0f;
     const float u_scale = fast ? pr.scale_upd / pr.scale_intra : 1.0f;
@@ -187,14 +198,31 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
             const uint32_t off = jr * 128 + ((((c0 + i) / 8) ^ (jr & 7)) << 4);
             put(S.x[0], S.x[OUT ? 1 : 0], S.x[OUT ? 2 : 0], off, X + i, f);
         }
+    };
+    // q's and k's pieces; f: K' 's factor of a row
+    auto put_qk = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t off = voff + i * 64 * 128;
+            if (OUT) put(S.q[0], S.q[OUT ? 1 : 0], S.q[OUT ? 2 : 0], off, rq[i], 1.0f);
+            put(S.k[0], S.k[1], S.k[2], off, rk[i], f(vr + 64 * i));
+        }
         tc::fence_async_smem();
-        arrive(S.xr);
     };
     if (!issuer && nchunk > 0) {
-        if (OUT && has_in) store_x(min(C, n - first(0)));
+        const int m = min(C, n - first(0));
+        if (OUT && has_in) store_x(m);
+        put_qk([&](int r) {
+            return fast ? decay_pow(base, rev ? r - 63 : 63 - r) * pr.scale_intra
+                   : OUT ? 1.0f : decay_pow(base, rev ? r + 1 : max(m - 1 - r, 0)) * pr.scale_upd;
+        });
     }
-    __syncthreads();  // tables, barriers, tensor memory's address
+    __syncthreads();  // tables, barriers, tensor memory's address, the first chunk's pieces
     tc::fence_after();
+    if (!issuer && nchunk > 0) {
+        if (OUT && has_in) arrive(S.xr);
+        arrive(S.kt);
+    }
     const uint32_t tmem = S.tmem;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
 
@@ -295,24 +323,17 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
         const int a = first(ci), m = min(C, n - a);
         const bool more = ci + 1 < nchunk, update = more || has_out, with_x = OUT && (ci > 0 || has_in);
         // the tiles' pieces
-        {
-            float rq[2][8], rk[2][8];
+        if (ci > 0) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (OUT) fetch(0, i, a, m, rq[i]);
                 fetch(1, i, a, m, rk[i]);
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = vr + 64 * i;
-                const uint32_t off = voff + i * 64 * 128;
-                if (OUT) put(S.q[0], S.q[OUT ? 1 : 0], S.q[OUT ? 2 : 0], off, rq[i], 1.0f);
-                put(S.k[0], S.k[1], S.k[2], off, rk[i],
-                    fast ? S.col[r] : OUT ? 1.0f : S.pw[rev ? r + 1 : max(m - 1 - r, 0)] * pr.scale_upd);
-            }
+            put_qk([&](int r) {
+                return fast ? S.col[r] : OUT ? 1.0f : S.pw[rev ? r + 1 : max(m - 1 - r, 0)] * pr.scale_upd;
+            });
+            arrive(S.kt);
         }
-        tc::fence_async_smem();
-        arrive(S.kt);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float rv[8];
@@ -345,14 +366,13 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
             const bool live = wg <= wq && 32 * j < m;
             float v[32];
             if (live) {
-                tc::tmem_ld32(lanes + 32 * j, v);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    float s[16];
-                    tc::tmem_ld16(lanes + 128 + 32 * j + 16 * half, s);
+                    float y[16], s[16];
+                    tc::tmem_ld16_pair(lanes + 32 * j + 16 * half, y, lanes + 128 + 32 * j + 16 * half, s);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
-                        const float2 x = add2(f2(v[16 * half + i], v[16 * half + i + 1]), f2(s[i], s[i + 1]));
+                        const float2 x = add2(f2(y[i], y[i + 1]), f2(s[i], s[i + 1]));
                         v[16 * half + i] = x.x;
                         v[16 * half + i + 1] = x.y;
                     }
@@ -419,19 +439,22 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
             tc::fence_before();
             arrive(S.pr);
         }
-        if (more) prefetch(ci + 1);
+        if (more) prefetch(ci + 1, OUT ? 0 : 1);
         if (update) {
             if (!wait(S.u, ci)) break;
             tc::fence_after();
             const float fx = S.pw[m];
             const float c = fast && !rev && m < C ? decay_pow(base, m - 64) * u_scale : u_full;
             float y[8], s[8];
-            tc::tmem_ld8(lanes + kColU + c0, y);
-            tc::tmem_ld8(lanes + kColU + 64 + c0, s);
+            tc::tmem_ld8_pair(lanes + kColU + c0, y, lanes + kColU + 64 + c0, s);
 #pragma unroll
             for (int i = 0; i < NX; ++i) X[i] = fmaf(fx, X[i], c * (y[i] + s[i]));
             tc::fence_before();
-            if (OUT && more) store_x(min(C, n - first(ci + 1)));
+            if (OUT && more) {
+                store_x(min(C, n - first(ci + 1)));
+                tc::fence_async_smem();
+                arrive(S.xr);
+            }
         }
         if (OUT) {
             if (!wait(S.o, ci)) break;
@@ -440,14 +463,15 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
             const float f = fast ? S.row[row] : 1.0f;
             char* dst = pr.out + ((((size_t)b * p.T + t0 + a + row) * p.H + h) * d + wg * 16) * 4;
             const int here = d - wg * 16;               // channels there are
+            float y[16], s[16];
+            tc::tmem_ld16_pair(lanes + kColO + wg * 16, y, lanes + kColO + 64 + wg * 16, s);
+            tc::fence_before();
+            arrive(S.of);
 #pragma unroll
             for (int i = 0; i < 16; i += 8) {
-                float y[8], s[8];
-                tc::tmem_ld8(lanes + kColO + wg * 16 + i, y);
-                tc::tmem_ld8(lanes + kColO + 64 + wg * 16 + i, s);
                 uint32_t o[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint((y[e] + s[e]) * f);
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint((y[i + e] + s[i + e]) * f);
                 if (row >= m) continue;
                 if (P.wide_out) {
                     if (i < here) st_global_32(dst + 4 * i, o);
@@ -456,8 +480,6 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
                     if (i + 4 < here) *reinterpret_cast<uint4*>(dst + 4 * i + 16) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
             }
-            tc::fence_before();
-            arrive(S.of);
         }
     }
     if (has_out && !issuer && ci == nchunk) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, d);
