@@ -50,6 +50,36 @@ cudaError_t ensure_smem(K kernel, std::atomic<int>& granted, int bytes) {
     return e;
 }
 
+// The same for each device: the limit belongs to a device's copy of the kernel.
+struct SmemGrants {
+    std::atomic<int> of[64] = {};
+};
+template <typename K>
+cudaError_t ensure_smem(K kernel, SmemGrants& granted, int bytes) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return ensure_smem(kernel, granted.of[dev], bytes);
+}
+
+// One kernel launch.  `follows`: it may begin while the stream's last kernel,
+// one of the same call, ends (passes.cuh).
+template <typename... P, typename... A>
+vrwkv_status launch(void (*kernel)(P...), const char* name, dim3 grid, int threads, int smem, bool follows, cudaStream_t s,
+                    const A&... args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = follows ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...), name);
+}
 }  // namespace api
 
 // The LayerNorm forward launch (layer_norm_api.cu); its arguments are checked.

@@ -21,6 +21,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "passes.cuh"
 
 namespace vrwkv {
 namespace decay {
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
     float* pw = sx + DP * LD;                // e^{-w n}, n = 0 .. C
     const Problem& pr = p.pr[blockIdx.x % p.nprob];
     const int hid = blockIdx.x / p.nprob, seg = hid % p.nseg, bh = hid / p.nseg, b = bh / p.H, h = bh % p.H;
+    next_pass();
     if (!pr.out && seg == pr.skip) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int D = p.D;
@@ -221,6 +223,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
     // this warp's rows of a chunk and first v channel of its output; its v and first k channel of X^T
     const int mt = warp % 2, c0 = (warp / 2) * NT * 8;
     const int um = (warp % UM) * 16, u0 = (warp / UM) * UT * 8;
+    last_pass();
     float X[UT][4];                          // rows um + g, um + g + 8, columns u0 + 8 i + 2 t, + 1
 #pragma unroll
     for (int i = 0; i < UT; ++i)
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kResident)
         for (int e = 0; e < 4; ++e) {
             const int dv = um + g + (e >> 1) * 8, dk = u0 + 8 * i + 2 * t + (e & 1);
             X[i][e] = pr.x_in && dv < D && dk < D
-                          ? __ldg(pr.x_in + xo + (pr.x_in_t ? (size_t)dv * D + dk : (size_t)dk * D + dv)) : 0.f;
+                          ? __ldcg(pr.x_in + xo + (pr.x_in_t ? (size_t)dv * D + dk : (size_t)dk * D + dv)) : 0.f;
         }
 
     // a thread's part of a chunk's q, k, v tiles, zero past the chunk's tokens and the head's channels
@@ -441,7 +444,7 @@ __device__ __forceinline__ void chain(const ChainParams& p, const ChainProblem& 
     for (int s0 = 0; s0 < reads; s0 += kAhead) {
 #pragma unroll
         for (int s = 0; s < kAhead; ++s)
-            if (s0 + s < reads) own[s] = *reinterpret_cast<const V*>(u + (size_t)(seg + s * step) * p.dd);
+            if (s0 + s < reads) own[s] = __ldcg(reinterpret_cast<const V*>(u + (size_t)(seg + s * step) * p.dd));
 #pragma unroll
         for (int s = 0; s < kAhead; ++s) {
             if (s0 + s >= reads) break;
@@ -462,11 +465,13 @@ __device__ __forceinline__ void chain(const ChainParams& p, const ChainProblem& 
 }
 
 __global__ void __launch_bounds__(256) decay_chain_kernel(const ChainParams p) {
+    next_pass();
     const ChainProblem& pr = p.pr[blockIdx.z];
     const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
     const int x = blockIdx.y * 256 + threadIdx.x;
     const DecayBase w = decay_base(__ldg(p.w + h));
     const int n_seq = seq_tokens(p.lengths, b, p.T);
+    last_pass();
     if (p.dd % 4 == 0) {
         if (4 * x < p.dd) chain<float4>(p, pr, bh, 4 * x, w, n_seq);
     } else if (x < p.dd) {

@@ -164,23 +164,23 @@ size_t ws_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
 
 // ---- launches ----
 template <typename IO, int DP>
-vrwkv_status launch_dp(const decay::Params& p, long long ctas, cudaStream_t s) {
-    static std::atomic<int> granted{0};
+vrwkv_status launch_dp(const decay::Params& p, long long ctas, bool follows, cudaStream_t s) {
+    static SmemGrants granted;
     constexpr int smem = decay::Cfg<DP>::kSmemFloats * 4;
     const cudaError_t e = ensure_smem(decay::decay_attn_kernel<IO, DP>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    decay::decay_attn_kernel<IO, DP><<<(unsigned)ctas, decay::Cfg<DP>::kThreads, smem, s>>>(p);
-    return cuda_status(cudaGetLastError(), "decay_attn_kernel launch");
+    return launch(decay::decay_attn_kernel<IO, DP>, "decay_attn_kernel launch", dim3((unsigned)ctas),
+                  decay::Cfg<DP>::kThreads, smem, follows, s, p);
 }
 
 template <typename IO>
-vrwkv_status launch_io(const decay::Params& p, cudaStream_t s) {
+vrwkv_status launch_io(const decay::Params& p, bool follows, cudaStream_t s) {
     const long long ctas = (long long)p.B * p.H * p.nseg * p.nprob;
     if (ctas > INT_MAX / 4) return fail(VRWKV_ERR_UNSUPPORTED, "too many heads (B*H = %lld)", (long long)p.B * p.H);
     switch (padded_d(p.D)) {
-    case 32: return launch_dp<IO, 32>(p, ctas, s);
-    case 64: return launch_dp<IO, 64>(p, ctas, s);
-    default: return launch_dp<IO, 128>(p, ctas, s);
+    case 32: return launch_dp<IO, 32>(p, ctas, follows, s);
+    case 64: return launch_dp<IO, 64>(p, ctas, follows, s);
+    default: return launch_dp<IO, 128>(p, ctas, follows, s);
     }
 }
 
@@ -201,21 +201,22 @@ bool encode_tokens(CUtensorMap* m, const void* x, long long ld, int B, int T, in
 bool rows16(const void* x, long long ld, int es) { return aligned(x, 16) && ld * es % 16 == 0 && ld < (1LL << 36); }
 
 template <int D, bool OUT, int PIECES, int PP, bool PAD>
-vrwkv_status launch_tc_pad(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
-    static std::atomic<int> granted{0};
+vrwkv_status launch_tc_pad(const decay::TcParams& p, unsigned ctas, bool follows, cudaStream_t s) {
+    static SmemGrants granted;
     constexpr int smem = decay::tc_smem_bytes<D, OUT>();
     const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT, PIECES, PP, PAD>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    decay::decay_attn_tc_kernel<D, OUT, PIECES, PP, PAD><<<ctas, decay::tc_threads<D>(), smem, s>>>(p);
-    return cuda_status(cudaGetLastError(), "decay_attn_tc_kernel launch");
+    return launch(decay::decay_attn_tc_kernel<D, OUT, PIECES, PP, PAD>, "decay_attn_tc_kernel launch", dim3(ctas),
+                  decay::tc_threads<D>(), smem, follows, s, p);
 }
 template <int D, bool OUT, int PIECES, int PP>
-vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, cudaStream_t s) {
-    return OUT && p.p.D == D ? launch_tc_pad<D, OUT, PIECES, PP, !OUT>(p, ctas, s) : launch_tc_pad<D, OUT, PIECES, PP, true>(p, ctas, s);
+vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, bool follows, cudaStream_t s) {
+    return OUT && p.p.D == D ? launch_tc_pad<D, OUT, PIECES, PP, !OUT>(p, ctas, follows, s)
+                             : launch_tc_pad<D, OUT, PIECES, PP, true>(p, ctas, follows, s);
 }
 template <int PIECES, int PP>
-vrwkv_status launch_tc64(decay::TcParams& p, cudaStream_t s) {
-    static std::atomic<int> granted{0};
+vrwkv_status launch_tc64(decay::TcParams& p, bool follows, cudaStream_t s) {
+    static SmemGrants granted;
     constexpr int smem = decay::t64_smem_bytes();
     const cudaError_t e = ensure_smem(decay::decay_attn_tc64_kernel<PIECES, PP>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
@@ -227,17 +228,17 @@ vrwkv_status launch_tc64(decay::TcParams& p, cudaStream_t s) {
         left /= radix[i];
     }
     p.step[3] = left;
-    decay::decay_attn_tc64_kernel<PIECES, PP><<<ctas, decay::kT64Threads, smem, s>>>(p);
-    return cuda_status(cudaGetLastError(), "decay_attn_tc64_kernel launch");
+    return launch(decay::decay_attn_tc64_kernel<PIECES, PP>, "decay_attn_tc64_kernel launch", dim3(ctas),
+                  decay::kT64Threads, smem, follows, s, p);
 }
 template <bool OUT>
-vrwkv_status launch_tcf(const decay::TcParams& p, cudaStream_t s) {
-    static std::atomic<int> granted{0};
+vrwkv_status launch_tcf(const decay::TcParams& p, bool follows, cudaStream_t s) {
+    static SmemGrants granted;
     constexpr int smem = decay::tf_smem_bytes<OUT>();
     const cudaError_t e = ensure_smem(decay::decay_attn_tcf_kernel<OUT>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    decay::decay_attn_tcf_kernel<OUT><<<(unsigned)p.nitems, decay::kTfThreads, smem, s>>>(p);
-    return cuda_status(cudaGetLastError(), "decay_attn_tcf_kernel launch");
+    return launch(decay::decay_attn_tcf_kernel<OUT>, "decay_attn_tcf_kernel launch", dim3((unsigned)p.nitems),
+                  decay::kTfThreads, smem, follows, s, p);
 }
 
 // Operands of the tensor cores as one bfloat16 each (P, K~) from this many
@@ -247,19 +248,19 @@ vrwkv_status launch_tcf(const decay::TcParams& p, cudaStream_t s) {
 // product's rounding could stand out, and time is latency: two pieces, 1.00.
 constexpr long long kRoundedRows = 8192;
 
-vrwkv_status launch_tc_any(decay::TcParams& p, bool exact, cudaStream_t s) {
+vrwkv_status launch_tc_any(decay::TcParams& p, bool exact, bool follows, cudaStream_t s) {
     const unsigned n = (unsigned)p.nitems;
     const bool rounded = (long long)p.p.B * p.p.T * p.p.H >= kRoundedRows;
     if (p.p.pr[0].out && p.p.D <= 64) {
-        if (rounded) return exact ? launch_tc64<3, 1>(p, s) : launch_tc64<1, 1>(p, s);
-        return exact ? launch_tc64<3, 2>(p, s) : launch_tc64<2, 2>(p, s);
+        if (rounded) return exact ? launch_tc64<3, 1>(p, follows, s) : launch_tc64<1, 1>(p, follows, s);
+        return exact ? launch_tc64<3, 2>(p, follows, s) : launch_tc64<2, 2>(p, follows, s);
     }
     if (p.p.pr[0].out) {
-        if (rounded) return exact ? launch_tc<128, true, 3, 1>(p, n, s) : launch_tc<128, true, 1, 1>(p, n, s);
-        return exact ? launch_tc<128, true, 3, 2>(p, n, s) : launch_tc<128, true, 2, 2>(p, n, s);
+        if (rounded) return exact ? launch_tc<128, true, 3, 1>(p, n, follows, s) : launch_tc<128, true, 1, 1>(p, n, follows, s);
+        return exact ? launch_tc<128, true, 3, 2>(p, n, follows, s) : launch_tc<128, true, 2, 2>(p, n, follows, s);
     }
-    if (p.p.D <= 64) return exact ? launch_tc<64, false, 3, 2>(p, n, s) : launch_tc<64, false, 2, 2>(p, n, s);
-    return exact ? launch_tc<128, false, 3, 2>(p, n, s) : launch_tc<128, false, 2, 2>(p, n, s);
+    if (p.p.D <= 64) return exact ? launch_tc<64, false, 3, 2>(p, n, follows, s) : launch_tc<64, false, 2, 2>(p, n, follows, s);
+    return exact ? launch_tc<128, false, 3, 2>(p, n, follows, s) : launch_tc<128, false, 2, 2>(p, n, follows, s);
 }
 
 // Launch p's problems; with `tc`, on the tensor cores with its maps.
@@ -280,8 +281,9 @@ struct Launcher {
             if (src[i] == x && ld[i] == row) return i;
         return 0;  // no q: the state alone
     }
-    vrwkv_status run(const decay::Params& p, cudaStream_t s) {
-        if (!tc) return dtype == VRWKV_F32 ? launch_io<float>(p, s) : launch_io<__nv_bfloat16>(p, s);
+    // follows: behind the call's chain kernel
+    vrwkv_status run(const decay::Params& p, bool follows, cudaStream_t s) {
+        if (!tc) return dtype == VRWKV_F32 ? launch_io<float>(p, follows, s) : launch_io<__nv_bfloat16>(p, follows, s);
         const long long ctas = (long long)p.B * p.H * p.nseg * p.nprob;
         if (ctas > INT_MAX) return fail(VRWKV_ERR_UNSUPPORTED, "too many heads (B*H = %lld)", (long long)p.B * p.H);
         t.p = p;
@@ -291,8 +293,8 @@ struct Launcher {
             t.mv[i] = map_of(p.pr[i].v, p.pr[i].ldv);
         }
         t.nitems = (int)ctas;
-        if (dtype == VRWKV_F32) return p.pr[0].out ? launch_tcf<true>(t, s) : launch_tcf<false>(t, s);
-        return launch_tc_any(t, exact, s);
+        if (dtype == VRWKV_F32) return p.pr[0].out ? launch_tcf<true>(t, follows, s) : launch_tcf<false>(t, follows, s);
+        return launch_tc_any(t, exact, follows, s);
     }
 };
 
@@ -328,8 +330,8 @@ Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long*
 
 vrwkv_status launch_chain(const decay::ChainParams& p, int bh, int nprob, cudaStream_t s) {
     const int per = p.dd % 4 == 0 ? 1024 : 256;  // elements of a CTA
-    decay::decay_chain_kernel<<<dim3((unsigned)bh, (unsigned)((p.dd + per - 1) / per), (unsigned)nprob), 256, 0, s>>>(p);
-    return cuda_status(cudaGetLastError(), "decay_chain_kernel launch");
+    return launch(decay::decay_chain_kernel, "decay_chain_kernel launch",
+                  dim3((unsigned)bh, (unsigned)((p.dd + per - 1) / per), (unsigned)nprob), 256, 0, true, s, p);
 }
 
 bool vec_ok(const void* p, long long ld, int es) { return aligned(p, 4 * es) && ld % 4 == 0; }
@@ -401,7 +403,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     if (cut.nseg > 1) {
         pr.x_out = ws;
         pr.skip = state_out ? -1 : cut.nseg - 1;
-        st = attn.run(p, s);
+        st = attn.run(p, false, s);
         if (st != VRWKV_OK) return st;
         decay::ChainParams c = {};
         c.pr[0] = {ws, state, state_out, 0};
@@ -422,7 +424,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
         pr.x_out = state_out;
     }
     pr.out = static_cast<char*>(out);
-    st = attn.run(p, s);
+    st = attn.run(p, cut.nseg > 1, s);
     if (st == VRWKV_OK) set_last_kernel(attn.kernel(D));
     return st;
 }
@@ -503,7 +505,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
         c.scale_upd = scale;
         c.reverse = 1;
         p.nprob = 2;
-        st = attn.run(p, s);
+        st = attn.run(p, false, s);
         if (st != VRWKV_OK) return st;
         decay::ChainParams cp = {};
         cp.pr[0] = {ws, state, nullptr, 0};
@@ -528,7 +530,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     // gk: (v, g, q) in reversed time on (dL/dS)^T; gv: (k, q, g) on dL/dS
     p.pr[1] = {V, G, Q, static_cast<char*>(gk), ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale, -1};
     p.pr[2] = {K, Q, G, static_cast<char*>(gv), ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale, -1};
-    st = attn.run(p, s);
+    st = attn.run(p, cut.nseg > 1, s);
     if (st == VRWKV_OK) set_last_kernel(attn.kernel(D));
     return st;
 }
@@ -577,14 +579,14 @@ vrwkv_status vrwkv_decay_attn_step(const void* q, const void* k, const void* v, 
     if (!p.err) return fail(VRWKV_ERR_CUDA, "cannot locate the device error word");
     const dim3 grid((unsigned)B, (unsigned)H, (unsigned)((D + decay::kStepCols - 1) / decay::kStepCols));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto launch = [&](auto io) {
+    auto step = [&](auto io) {
         using IO = decltype(io);
         if (D <= 32) decay::decay_step_kernel<IO, 2><<<grid, decay::kStepThreads, 0, s>>>(p);
         else if (D <= 64) decay::decay_step_kernel<IO, 4><<<grid, decay::kStepThreads, 0, s>>>(p);
         else decay::decay_step_kernel<IO, 8><<<grid, decay::kStepThreads, 0, s>>>(p);
     };
-    if (dtype == VRWKV_F32) launch(float{});
-    else launch(__nv_bfloat16{});
+    if (dtype == VRWKV_F32) step(float{});
+    else step(__nv_bfloat16{});
     st = cuda_status(cudaGetLastError(), "decay_step_kernel launch");
     if (st == VRWKV_OK) set_last_kernel("decay_step_kernel");
     return st;

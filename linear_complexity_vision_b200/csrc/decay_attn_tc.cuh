@@ -193,7 +193,7 @@ __device__ __forceinline__ void load_x(float (&X)[NX], const float* x, bool tran
     if (transposed) {
 #pragma unroll
         for (int i = 0; i < NX; i += 4) {
-            const float4 y = __ldg(reinterpret_cast<const float4*>(x + (i < here ? jr * d + c0 + i : 0)));
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(x + (i < here ? jr * d + c0 + i : 0)));
             X[i] = i < here ? y.x : 0.f;
             X[i + 1] = i < here ? y.y : 0.f;
             X[i + 2] = i < here ? y.z : 0.f;
@@ -202,7 +202,7 @@ __device__ __forceinline__ void load_x(float (&X)[NX], const float* x, bool tran
     } else {
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const float y = __ldg(x + (i < here ? (c0 + i) * d + jr : 0));
+            const float y = __ldcg(x + (i < here ? (c0 + i) * d + jr : 0));
             X[i] = i < here ? y : 0.f;
         }
     }
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     const int prob = blockIdx.x % p.nprob;
     const Problem& pr = p.pr[prob];
     const int sid = blockIdx.x / p.nprob, seg = sid % p.nseg, bh = sid / p.nseg, b = bh / p.H, h = bh % p.H;
+    next_pass();
     if (!OUT && seg == pr.skip) return;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, quad = warp & 3, wg = warp >> 2;
     const float w = __ldg(p.w + h);
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     const int jr = D == 64 ? (quad & 1) * 32 + lane : quad * 32 + lane;
     const int c0 = D == 64 ? ((quad >> 1) * 2 + wg) * NX : wg * NX;
     float X[NX];
+    last_pass();
     if (has_in && !issuer) {
         load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, d);
     } else {

@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         }
     } else if (warp < 20) {
         // ---- the state: thread = half a row of X^T (v channel jr, k channels c0 ..); U has its rows twice ----
+        last_pass();
         constexpr int NX = 32;
         const int quad = warp & 3, jr = (quad & 1) * 32 + lane, c0 = (quad >> 1) * NX;
         const uint32_t lanes = S.tmem + ((uint32_t)(quad * 32) << 16) + 192 + c0;

@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     const int prob = blockIdx.x % p.nprob;
     const Problem& pr = p.pr[prob];
     const int sid = blockIdx.x / p.nprob, seg = sid % p.nseg, bh = sid / p.nseg, b = bh / p.H, h = bh % p.H;
+    next_pass();
     if (!OUT && seg == pr.skip) return;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, quad = warp & 3, wg = warp >> 2;
     const bool issuer = warp == NW;
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     constexpr int NX = D * D / kWork;
     const int jr = (quad & 1) * 32 + lane, c0 = ((quad >> 1) * 4 + wg) * NX;
     float X[NX];
+    last_pass();
     if (has_in && !issuer) {
         load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, d);
     } else {

@@ -211,8 +211,9 @@ vrwkv_status vrwkv_layer_norm_bwd(const void* x, const float* gamma, const float
     st = cuda_status(cudaGetLastError(), "layer_norm_bwd_kernel launch");
     if (st != VRWKV_OK) return st;
     if (ggamma) {
-        layer_norm_wgrad_kernel<<<(2 * C + kLnWgradCols - 1) / kLnWgradCols, 1024, 0, s>>>(p.part, pl.grid, C, ggamma, gbeta);
-        st = cuda_status(cudaGetLastError(), "layer_norm_wgrad_kernel launch");
+        st = launch(layer_norm_wgrad_kernel, "layer_norm_wgrad_kernel launch",
+                    dim3((unsigned)((2 * C + kLnWgradCols - 1) / kLnWgradCols)), 1024, 0, true, s, (const float*)p.part, pl.grid, C,
+                    ggamma, gbeta);
         if (st != VRWKV_OK) return st;
     }
     set_last_kernel("layer_norm_bwd_kernel");

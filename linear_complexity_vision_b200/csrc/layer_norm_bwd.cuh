@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "layer_norm.cuh"
+#include "passes.cuh"
 #include "qshift.cuh"
 
 namespace vrwkv {
@@ -74,6 +75,7 @@ template <typename IO, int VPL>
 __global__ void __launch_bounds__(32 * kLnBwdWarps, ln_bwd_ctas<IO>(VPL)) layer_norm_bwd_warp_kernel(const LayerNormBwdParams p) {
     using V = Vec16<IO>;
     constexpr int N = V::N, N2 = N / 2, E = VPL * N;  // channels of a lane: vectors lane + 32 k
+    next_pass();
     extern __shared__ __align__(16) float sg[];  // gamma, then the CTA's partial rows: max(1, 2) * C floats
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nv = p.C / N;
@@ -176,6 +178,7 @@ template <typename IO, bool VEC, int NV>
 __global__ void __launch_bounds__(1024) layer_norm_bwd_kernel(const LayerNormBwdParams p) {
     using V = LnVec<IO, VEC>;
     constexpr int N = V::N;
+    next_pass();
     __shared__ float red[2][32][2];
     const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
     const int nv = p.C / N;
@@ -266,9 +269,10 @@ __global__ void __launch_bounds__(1024) layer_norm_wgrad_kernel(const float* par
     const int tid = threadIdx.x, col = tid % kLnWgradCols, group = tid / kLnWgradCols;
     const int c = blockIdx.x * kLnWgradCols + col;
     float s = 0.f;
+    last_pass();
     if (c < 2 * C) {
 #pragma unroll 8
-        for (int i = group; i < n; i += 1024 / kLnWgradCols) s += __ldg(part + (size_t)i * 2 * C + c);
+        for (int i = group; i < n; i += 1024 / kLnWgradCols) s += __ldcg(part + (size_t)i * 2 * C + c);
     }
     s += __shfl_xor_sync(0xffffffffu, s, 8);
     s += __shfl_xor_sync(0xffffffffu, s, 16);
