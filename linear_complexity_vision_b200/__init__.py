@@ -560,13 +560,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _empty_rows(t, shape, dtype, device):
-    return _torch.empty_like(t) if t.is_contiguous() else _torch.empty(shape, dtype=dtype, device=device)
+def _empty_rows(t, shape):
+    return _torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape)
 
 
-def _workspace(key, size, workspace, device):
+def _workspace(key, size, workspace, device, f32):
     """(pointer, bytes, tensor) of the caller's workspace, or of a new one of
-    the size remembered under key (size(): the library's answer)."""
+    the size remembered under key (size(): the library's answer); f32: any
+    float32 tensor there."""
     if workspace is not None:
         _require(workspace, "workspace")
         if workspace.device != device:
@@ -578,7 +579,7 @@ def _workspace(key, size, workspace, device):
         need = _ws_need[key] = int(size())
     if not need:
         return None, 0, None
-    t = _torch.empty(need, dtype=_torch.uint8, device=device)
+    t = f32.new_empty((need + 3) // 4)
     return t.data_ptr(), need, t
 
 
@@ -639,14 +640,14 @@ def decay_attn_fwd(q, k, v, w, heads: int, scale: float = 1.0, state=None, lengt
     if out is not None:
         _require_like("out", out, shape, dtype, dev, "q")
     else:
-        out = _empty_rows(q, shape, dtype, dev)
+        out = _empty_rows(q, shape)
     if state_out is None and want_state:
-        state_out = _torch.empty(states, dtype=_torch.float32, device=dev)
+        state_out = w.new_empty(states)
     lib = load_library()
 
     def call():
         ws, n, keep = _workspace((B, T, heads, D, code, 0),
-                                 lambda: lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 0), workspace, dev)
+                                 lambda: lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 0), workspace, dev, w)
         return lib.vrwkv_decay_attn_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, w.data_ptr(), _ptr(state), _ptr(lengths), scale,
             out.data_ptr(), _ptr(state_out), B, T, heads, D, code, ws, n, _torch._C._cuda_getCurrentRawStream(dev.index))
@@ -679,8 +680,8 @@ def decay_attn_bwd(q, k, v, w, heads: int, gy, scale: float = 1.0, state=None, g
     if lengths is not None:
         _require_ints("lengths", lengths, B, dev)
     if out is None:
-        gq, gk, gv = (_torch.empty(shape, dtype=dtype, device=dev) for _ in range(3))
-        gs = None if state is None else _torch.empty(states, dtype=_torch.float32, device=dev)
+        gq, gk, gv = q.new_empty(shape), q.new_empty(shape), q.new_empty(shape)
+        gs = None if state is None else w.new_empty(states)
     else:
         gq, gk, gv, gs = out
         for n, t in (("gq", gq), ("gk", gk), ("gv", gv)):
@@ -691,7 +692,7 @@ def decay_attn_bwd(q, k, v, w, heads: int, gy, scale: float = 1.0, state=None, g
 
     def call():
         ws, n, keep = _workspace((B, T, heads, D, code, 1),
-                                 lambda: lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 1), workspace, dev)
+                                 lambda: lib.vrwkv_decay_attn_workspace_bytes(B, T, heads, D, code, 1), workspace, dev, w)
         return lib.vrwkv_decay_attn_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), gy.data_ptr(), ldq, ldk, ldv, ldg, w.data_ptr(), _ptr(state),
             _ptr(gstate), _ptr(lengths), scale, gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gs), B, T, heads, D,
@@ -723,7 +724,7 @@ def decay_attn_step(q, k, v, w, heads: int, state, slots=None, scale: float = 1.
     if slots is not None:
         _require_ints("slots", slots, B, dev)
     if out is None:
-        out = _empty_rows(q, shape, dtype, dev)
+        out = _empty_rows(q, shape)
     else:
         _require_like("out", out, shape, dtype, dev, "q")
     lib = load_library()
@@ -762,7 +763,7 @@ def layer_norm_fwd(x, gamma, beta, eps: float = 1e-5, stats: bool = True, out=No
         _require_like("out", out, shape, dtype, dev, "x")
     mean = rstd = None
     if stats:
-        mean = _torch.empty(shape[:-1], dtype=_torch.float32, device=dev)
+        mean = gamma.new_empty(shape[:-1])
         rstd = _torch.empty_like(mean)
     lib = load_library()
     _check(_on_device(dev, lambda: lib.vrwkv_layer_norm_fwd(
@@ -802,7 +803,7 @@ def layer_norm_bwd(x, gamma, mean, rstd, gy, weight_grads: bool = True, out=None
 
     def call():
         ws, n, keep = (None, 0, None) if not weight_grads else _workspace(
-            (rows, C, code), lambda: lib.vrwkv_layer_norm_bwd_workspace_bytes(rows, C, code), workspace, dev)
+            (rows, C, code), lambda: lib.vrwkv_layer_norm_bwd_workspace_bytes(rows, C, code), workspace, dev, gamma)
         return lib.vrwkv_layer_norm_bwd(
             x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), gy.data_ptr(), out.data_ptr(),
             _ptr(ggamma), _ptr(gbeta), rows, C, code, ws, n, _torch._C._cuda_getCurrentRawStream(dev.index))

@@ -150,16 +150,17 @@ bool tc_disabled() {
 
 size_t state_floats(int B, int H, int D, int nseg) { return (size_t)B * H * nseg * D * D; }
 
-// The larger of what the two kernels' cuts need: which of them runs also
-// depends on the tensors' alignment.
+// What the cut needs of the kernel that the sizes go to.
 size_t ws_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
-    size_t need = 0;
-    for (int tc = 0; tc <= (tc_sizes(T, D, dtype) ? 1 : 0); ++tc) {
-        const Cut c = plan(B, T, H, D, dtype, backward ? 3 : 1, tc != 0);
-        if (c.nseg > 1)
-            need = std::max(need, ((backward ? 2 : 1) * state_floats(B, H, D, c.nseg) * 4 + 255) / 256 * 256);
-    }
-    return need;
+    const Cut c = plan(B, T, H, D, dtype, backward ? 3 : 1, tc_sizes(T, D, dtype));
+    return c.nseg > 1 ? ((backward ? 2 : 1) * state_floats(B, H, D, c.nseg) * 4 + 255) / 256 * 256 : 0;
+}
+// The cut of the kernel that runs: where alignment keeps it from the one of the
+// sizes, in as many segments as the workspace has room for.
+Cut cut_for(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward, bool tc, size_t workspace) {
+    const Cut c = plan(B, T, H, D, dtype, backward ? 3 : 1, tc);
+    const size_t most = workspace / ((backward ? 2 : 1) * state_floats(B, H, D, 1) * 4);
+    return (size_t)c.nseg <= most ? c : cut_into(T, (int)std::max<size_t>(most, 1));
 }
 
 // ---- launches ----
@@ -377,7 +378,7 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     const long long lds[3] = {ldq, ldk, ldv};
     Launcher attn =
         make_launcher(dtype, srcs, lds, 3, dsts, 1, state, nullptr, state_out != nullptr, B, T, H, D);
-    const Cut cut = plan(B, T, H, D, dtype, 1, attn.tc);
+    const Cut cut = cut_for(B, T, H, D, dtype, false, attn.tc, need);
     decay::Params p = {};
     p.w = w;
     p.lengths = lengths;
@@ -464,7 +465,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     const long long lds[4] = {ldq, ldk, ldv, ldg};
     Launcher attn =
         make_launcher(dtype, srcs, lds, 4, dsts, 3, state, gstate, gstate_in != nullptr, B, T, H, D);
-    const Cut cut = plan(B, T, H, D, dtype, 3, attn.tc);
+    const Cut cut = cut_for(B, T, H, D, dtype, true, attn.tc, need);
     decay::Params p = {};
     p.w = w;
     p.lengths = lengths;
