@@ -465,9 +465,10 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  *            none).
  *   workspace  device memory of at least vrwkv_decay_attn_workspace_bytes(B,
  *            T, H, D, dtype, backward) bytes, 256-byte aligned (NULL if that
- *            is 0): the states at the cuts of long sequences.  Its contents
- *            need no preparation.  Calls that may run at the same time need
- *            separate workspaces.
+ *            is 0): the states at the cuts of long sequences and, for
+ *            bfloat16 heads above 32 channels of no multiple of 8, copies of
+ *            the tensors.  Its contents need no preparation.  Calls that may
+ *            run at the same time need separate workspaces.
  * Limits: D <= 128 (UNSUPPORTED above).
  * Arithmetic: sums, decays and states in float32, products on the tensor
  *   cores from operands split into parts; outputs rounded once.
@@ -478,10 +479,10 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  *              meet v are in two parts too; calls of B*T*H >= 8192 may round
  *              them to one bfloat16: in outputs these roundings, half a step each
  *              and independent, weigh as much as the final one.
- *   Heads of a multiple of 8 channels (float32: 36 to 64, a multiple of 4) in
- *   tensors whose rows, outputs and states are 16-byte aligned take the
- *   fifth-generation tensor cores from 17 to 97 tokens on (by type and D), the
- *   rest a kernel for any size.  On the former, where |w| <= 1/2, sums carry
+ *   Heads of a multiple of 8 channels (float32: 36 to 64, a multiple of 4;
+ *   bfloat16 above 32: any) in tensors whose rows, outputs and states are
+ *   16-byte aligned take the fifth-generation tensor cores from 17 to 97
+ *   tokens on (by type and D), the rest a kernel for any size.  On the former, where |w| <= 1/2, sums carry
  *   factors within e^+-32: safe for outputs of magnitudes from 1e-24 to 1e24.
  *   The same call on the same alignments gives the same bits; a sequence's
  *   bits may differ between batches of other sizes.

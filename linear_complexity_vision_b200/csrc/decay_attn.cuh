@@ -49,6 +49,7 @@ struct Params {
     const float* w;         // (H)
     const int* lengths;     // (B) or nullptr
     int B, T, H, D;
+    int S;                  // a state is (S, S): D, but for spread heads (decay_pack.cuh)
     int seg_tokens, nseg;   // tokens of a segment, segments of a sequence
     int nprob;              // problems of this launch; CTA x: problem x % nprob of segment x / nprob
     int vec;                // rows can be read and written 4 elements at a time

@@ -11,6 +11,7 @@
 #include "decay_attn_tc.cuh"
 #include "decay_attn_tc64.cuh"
 #include "decay_attn_tcf.cuh"
+#include "decay_pack.cuh"
 
 namespace {
 
@@ -150,10 +151,32 @@ bool tc_disabled() {
 
 size_t state_floats(int B, int H, int D, int nseg) { return (size_t)B * H * nseg * D * D; }
 
+// bfloat16 heads that are spread to whole 16-byte vectors first (decay_pack.cuh):
+// how wide, or 0.  Measured, us, forward (spread : as they are), for 8, 160 and
+// 1024 heads:
+//   D = 27  T = 200  13.7 : 25.3  33.7 : 28.1  111 : 78
+//   D = 45  T = 64   11.0 : 14.2  17.8 : 16.6  49.8 : 48.8
+//           T = 96   11.1 : 21.2  20.5 : 24.6  64.5 : 74.8
+//   D = 89  T = 32   12.0 : 8.9   19.7 : 16.1  63.2 : 55.5
+//           T = 48   12.0 : 17.7  20.8 : 33.1  76.3 : 117
+// (float32, D = 45, T = 200: 23.1 : 41.7, 60.8 : 50.7, 240 : 172, as they are.)
+int spread_width(int T, int D, vrwkv_dtype dtype) {
+    return dtype == VRWKV_BF16 && D > 32 && D % 8 != 0 && T > (D <= 64 ? 64 : 32) ? (D + 7) / 8 * 8 : 0;
+}
+size_t spread_bytes(int B, int T, int H, int W) {  // of a tensor
+    return ((size_t)B * T * H * W * 2 + 255) / 256 * 256;
+}
+
 // What the cut needs of the kernel that the sizes go to.
-size_t ws_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
-    const Cut c = plan(B, T, H, D, dtype, backward ? 3 : 1, tc_sizes(T, D, dtype));
+size_t state_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
+    const int W = spread_width(T, D, dtype);
+    const Cut c = plan(B, T, H, D, dtype, backward ? 3 : 1, W || tc_sizes(T, D, dtype));
     return c.nseg > 1 ? ((backward ? 2 : 1) * state_floats(B, H, D, c.nseg) * 4 + 255) / 256 * 256 : 0;
+}
+// The states, then the spread inputs and outputs.
+size_t ws_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, bool backward) {
+    const int W = spread_width(T, D, dtype);
+    return state_bytes(B, T, H, D, dtype, backward) + (W ? (backward ? 7 : 4) * spread_bytes(B, T, H, W) : 0);
 }
 // The cut of the kernel that runs: where alignment keeps it from the one of the
 // sizes, in as many segments as the workspace has room for.
@@ -212,7 +235,7 @@ vrwkv_status launch_tc_pad(const decay::TcParams& p, unsigned ctas, bool follows
 }
 template <int D, bool OUT, int PIECES, int PP>
 vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, bool follows, cudaStream_t s) {
-    return OUT && p.p.D == D ? launch_tc_pad<D, OUT, PIECES, PP, !OUT>(p, ctas, follows, s)
+    return OUT && p.p.D == D && p.p.S == D ? launch_tc_pad<D, OUT, PIECES, PP, !OUT>(p, ctas, follows, s)
                              : launch_tc_pad<D, OUT, PIECES, PP, true>(p, ctas, follows, s);
 }
 template <int PIECES, int PP>
@@ -329,6 +352,43 @@ Launcher make_launcher(vrwkv_dtype dtype, const void* const* x, const long long*
     return l;
 }
 
+// A call's tensors spread to heads of W channels in the workspace.
+struct Spread {
+    int W, ni, no;
+    decay::PackParams in, out;
+    long long ld;  // of the spread rows
+
+    void init(int W_, char* ws, const void* const* x, const long long* lds, int n, void* const* y, int m, int B,
+              int T, int H, int D) {
+        W = W_;
+        ni = n;
+        no = m;
+        ld = (long long)H * W;
+        const size_t each = spread_bytes(B, T, H, W);
+        in = {};
+        in.heads = (long long)B * T * H;
+        in.H = H;
+        in.D = D;
+        in.W = W;
+        out = in;
+        for (int i = 0; i < n; ++i, ws += each) {
+            in.src[i] = static_cast<const char*>(x[i]);
+            in.dst[i] = ws;
+            in.ld[i] = lds[i];
+        }
+        for (int i = 0; i < m; ++i, ws += each) {
+            out.src[i] = ws;
+            out.dst[i] = static_cast<char*>(y[i]);
+            out.ld[i] = (long long)H * D;
+        }
+    }
+    vrwkv_status run(bool to_wide, cudaStream_t s) const {
+        const unsigned x = (unsigned)std::min<long long>((in.heads + 31) / 32, 8LL * sm_count());
+        return to_wide ? launch(decay::decay_pack_kernel<true>, "decay_pack_kernel launch", dim3(x, (unsigned)ni), 256, 0, false, s, in)
+                       : launch(decay::decay_pack_kernel<false>, "decay_pack_kernel launch", dim3(x, (unsigned)no), 256, 0, false, s, out);
+    }
+};
+
 vrwkv_status launch_chain(const decay::ChainParams& p, int bh, int nprob, cudaStream_t s) {
     const int per = p.dd % 4 == 0 ? 1024 : 256;  // elements of a CTA
     return launch(decay::decay_chain_kernel, "decay_chain_kernel launch",
@@ -376,30 +436,50 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
     const void* srcs[3] = {q, k, v};
     const void* dsts[1] = {out};
     const long long lds[3] = {ldq, ldk, ldv};
-    Launcher attn =
-        make_launcher(dtype, srcs, lds, 3, dsts, 1, state, nullptr, state_out != nullptr, B, T, H, D);
-    const Cut cut = cut_for(B, T, H, D, dtype, false, attn.tc, need);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t for_states = state_bytes(B, T, H, D, dtype, false);
+    Spread wide = {};
+    Launcher attn;
+    if (const int W = spread_width(T, D, dtype)) {
+        void* const outs_[1] = {out};
+        wide.init(W, static_cast<char*>(workspace) + for_states, srcs, lds, 3, outs_, 1, B, T, H, D);
+        const long long wlds[3] = {wide.ld, wide.ld, wide.ld};
+        attn = make_launcher(dtype, (const void* const*)wide.in.dst, wlds, 3, (const void* const*)wide.out.src, 1, state, nullptr,
+                             state_out != nullptr, B, T, H, W);
+        if (!attn.tc) wide.W = 0;
+    }
+    if (!wide.W) attn = make_launcher(dtype, srcs, lds, 3, dsts, 1, state, nullptr, state_out != nullptr, B, T, H, D);
+    const Cut cut = cut_for(B, T, H, D, dtype, false, attn.tc, for_states);
+    const char *Q = static_cast<const char*>(q), *K = static_cast<const char*>(k), *V = static_cast<const char*>(v);
+    char* O = static_cast<char*>(out);
+    if (wide.W) {
+        st = wide.run(true, s);
+        if (st != VRWKV_OK) return st;
+        Q = wide.in.dst[0], K = wide.in.dst[1], V = wide.in.dst[2];
+        O = const_cast<char*>(wide.out.src[0]);
+        ldq = ldk = ldv = wide.ld;
+    }
     decay::Params p = {};
     p.w = w;
     p.lengths = lengths;
     p.B = B;
     p.T = T;
     p.H = H;
-    p.D = D;
+    p.D = wide.W ? wide.W : D;
+    p.S = D;
     p.seg_tokens = cut.seg_tokens;
     p.nseg = cut.nseg;
     p.nprob = 1;
     p.vec = D % 4 == 0 && vec_ok(q, ldq, es) && vec_ok(k, ldk, es) && vec_ok(v, ldv, es) && vec_ok(out, C, es);
     decay::Problem& pr = p.pr[0];
-    pr.q = static_cast<const char*>(q);
-    pr.k = static_cast<const char*>(k);
-    pr.v = static_cast<const char*>(v);
+    pr.q = Q;
+    pr.k = K;
+    pr.v = V;
     pr.ldq = ldq;
     pr.ldk = ldk;
     pr.ldv = ldv;
     pr.scale_intra = pr.scale_inter = scale;
     pr.scale_upd = 1.0f;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     float* ws = static_cast<float*>(workspace);
     if (cut.nseg > 1) {
         pr.x_out = ws;
@@ -424,8 +504,9 @@ vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v, l
         pr.x_in = state;
         pr.x_out = state_out;
     }
-    pr.out = static_cast<char*>(out);
+    pr.out = O;
     st = attn.run(p, cut.nseg > 1, s);
+    if (st == VRWKV_OK && wide.W) st = wide.run(false, s);
     if (st == VRWKV_OK) set_last_kernel(attn.kernel(D));
     return st;
 }
@@ -463,25 +544,42 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     const void* srcs[4] = {q, k, v, gy};
     const void* dsts[3] = {gq, gk, gv};
     const long long lds[4] = {ldq, ldk, ldv, ldg};
-    Launcher attn =
-        make_launcher(dtype, srcs, lds, 4, dsts, 3, state, gstate, gstate_in != nullptr, B, T, H, D);
-    const Cut cut = cut_for(B, T, H, D, dtype, true, attn.tc, need);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t for_states = state_bytes(B, T, H, D, dtype, true);
+    Spread wide = {};
+    Launcher attn;
+    if (const int W = spread_width(T, D, dtype)) {
+        void* const outs_[3] = {gq, gk, gv};
+        wide.init(W, static_cast<char*>(workspace) + for_states, srcs, lds, 4, outs_, 3, B, T, H, D);
+        const long long wlds[4] = {wide.ld, wide.ld, wide.ld, wide.ld};
+        attn = make_launcher(dtype, (const void* const*)wide.in.dst, wlds, 4, (const void* const*)wide.out.src, 3, state, gstate,
+                             gstate_in != nullptr, B, T, H, W);
+        if (!attn.tc) wide.W = 0;
+    }
+    if (!wide.W) attn = make_launcher(dtype, srcs, lds, 4, dsts, 3, state, gstate, gstate_in != nullptr, B, T, H, D);
+    const Cut cut = cut_for(B, T, H, D, dtype, true, attn.tc, for_states);
+    const char *Q = static_cast<const char*>(q), *K = static_cast<const char*>(k), *V = static_cast<const char*>(v),
+               *G = static_cast<const char*>(gy);
+    char* grads[3] = {static_cast<char*>(gq), static_cast<char*>(gk), static_cast<char*>(gv)};
+    if (wide.W) {
+        st = wide.run(true, s);
+        if (st != VRWKV_OK) return st;
+        Q = wide.in.dst[0], K = wide.in.dst[1], V = wide.in.dst[2], G = wide.in.dst[3];
+        for (int i = 0; i < 3; ++i) grads[i] = const_cast<char*>(wide.out.src[i]);
+        ldq = ldk = ldv = ldg = wide.ld;
+    }
     decay::Params p = {};
     p.w = w;
     p.lengths = lengths;
     p.B = B;
     p.T = T;
     p.H = H;
-    p.D = D;
+    p.D = wide.W ? wide.W : D;
+    p.S = D;
     p.seg_tokens = cut.seg_tokens;
     p.nseg = cut.nseg;
     p.vec = D % 4 == 0 && vec_ok(q, ldq, es) && vec_ok(k, ldk, es) && vec_ok(v, ldv, es) && vec_ok(gy, ldg, es) &&
             vec_ok(gq, C, es) && vec_ok(gk, C, es) && vec_ok(gv, C, es);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const char* Q = static_cast<const char*>(q);
-    const char* K = static_cast<const char*>(k);
-    const char* V = static_cast<const char*>(v);
-    const char* G = static_cast<const char*>(gy);
     const float* s_in = state;   // X_in of the segments: S of the forward pass
     const float* g_in = gstate;  // and dL/dS of the reversed one
     float* g_out = gstate_in;
@@ -527,11 +625,12 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v, c
     }
     p.nprob = 3;
     // gq: (g, v, k) forward in time on S^T
-    p.pr[0] = {G, V, K, static_cast<char*>(gq), ldg, ldv, ldk, s_in, nullptr, 1, 1, 0, scale, scale, 1.0f, -1};
+    p.pr[0] = {G, V, K, grads[0], ldg, ldv, ldk, s_in, nullptr, 1, 1, 0, scale, scale, 1.0f, -1};
     // gk: (v, g, q) in reversed time on (dL/dS)^T; gv: (k, q, g) on dL/dS
-    p.pr[1] = {V, G, Q, static_cast<char*>(gk), ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale, -1};
-    p.pr[2] = {K, Q, G, static_cast<char*>(gv), ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale, -1};
+    p.pr[1] = {V, G, Q, grads[1], ldv, ldg, ldq, g_in, nullptr, 1, 1, 1, scale, 1.0f, scale, -1};
+    p.pr[2] = {K, Q, G, grads[2], ldk, ldq, ldg, g_in, g_out, 0, 0, 1, scale, 1.0f, scale, -1};
     st = attn.run(p, cut.nseg > 1, s);
+    if (st == VRWKV_OK && wide.W) st = wide.run(false, s);
     if (st == VRWKV_OK) set_last_kernel(attn.kernel(D));
     return st;
 }

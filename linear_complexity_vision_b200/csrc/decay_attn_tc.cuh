@@ -191,12 +191,12 @@ __device__ __forceinline__ void p_block(uint32_t taddr, int j, int d4, bool fast
     }
 }
 
-// Row jr of X^T, columns c0 .. c0 + NX, from a (d, d) state, zeros past d (a
-// multiple of 4; the state 16-byte aligned).  No load waits for a branch.
+// Row jr of X^T, columns c0 .. c0 + NX, from a (d, d) state, zeros past d (the
+// first state 16-byte aligned).  No load waits for a branch.
 template <int NX>
 __device__ __forceinline__ void load_x(float (&X)[NX], const float* x, bool transposed, int jr, int c0, int d) {
     const int here = jr < d ? d - c0 : 0;
-    if (transposed) {
+    if (transposed && d % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < NX; i += 4) {
             const float4 y = __ldcg(reinterpret_cast<const float4*>(x + (i < here ? jr * d + c0 + i : 0)));
@@ -208,7 +208,7 @@ __device__ __forceinline__ void load_x(float (&X)[NX], const float* x, bool tran
     } else {
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const float y = __ldcg(x + (i < here ? (c0 + i) * d + jr : 0));
+            const float y = __ldcg(x + (i < here ? (transposed ? jr * d + c0 + i : (c0 + i) * d + jr) : 0));
             X[i] = i < here ? y : 0.f;
         }
     }
@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     const int nchunk = (n + C - 1) / C;
     const bool has_in = pr.x_in != nullptr, has_out = pr.x_out != nullptr;
     const int d = PAD ? p.D : D;                        // channels there are; operands are zero past them
-    const size_t xo = ((size_t)bh * p.nseg + seg) * d * d;
+    const int sd = PAD ? p.S : D;                       // and of a state
+    const size_t xo = ((size_t)bh * p.nseg + seg) * sd * sd;
 
     if (tid == 0) {
         tc::mbar_init(&S.fa, 1);
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     float X[NX];
     last_pass();
     if (has_in && !issuer) {
-        load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, d);
+        load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, sd);
     } else {
 #pragma unroll
         for (int i = 0; i < NX; ++i) X[i] = 0.f;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
             }
         }
     }
-    if (has_out && !issuer && ci == nchunk) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, d);
+    if (has_out && !issuer && ci == nchunk) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, sd);
     if (OUT) {  // rows past the sequence's end
         for (int x = tid; x < (t_end - n) * (d / 8); x += kThreads)
             *reinterpret_cast<uint4*>(pr.out + (((size_t)b * p.T + t0 + n + x / (d / 8)) * p.H + h) * d * 2 +

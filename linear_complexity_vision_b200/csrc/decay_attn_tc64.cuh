@@ -95,7 +95,7 @@ struct T64Item {
         has_out = pr.x_out != nullptr;
     }
     __device__ __forceinline__ long long state_at(const Params& p) const {
-        return (((long long)b * p.H + h) * p.nseg + seg) * p.D * p.D;
+        return (((long long)b * p.H + h) * p.nseg + seg) * p.S * p.S;
     }
     __device__ __forceinline__ bool fast() const { return fabsf(w) <= kTcFastW; }
 };
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
             const long long xo = it.state_at(p);
             float X[NX];
             if (it.has_in) {
-                load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, p.D);
+                load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, p.S);
             } else {
 #pragma unroll
                 for (int i = 0; i < NX; ++i) X[i] = 0.f;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 if (more) okay = next_x(tokens(ci + 1), s ^ 1);
                 if (!okay) break;
             }
-            if (it.has_out && okay) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, p.D);
+            if (it.has_out && okay) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, p.S);
         }
     } else {
         // ---- issuer of a stream ----

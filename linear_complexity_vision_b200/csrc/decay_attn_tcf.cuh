@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     const int nchunk = (n + C - 1) / C;
     const bool has_in = pr.x_in != nullptr, has_out = pr.x_out != nullptr;
     const int d = p.D;                           // channels there are; operands are zero past them
-    const size_t xo = ((size_t)bh * p.nseg + seg) * d * d;
+    const size_t xo = ((size_t)bh * p.nseg + seg) * p.S * p.S;
 
     // chunk ci of the walk: its first token in the segment
     auto first = [&](int ci) { return (rev ? nchunk - 1 - ci : ci) * C; };
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     float X[NX];
     last_pass();
     if (has_in && !issuer) {
-        load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, d);
+        load_x(X, pr.x_in + xo, pr.x_in_t, jr, c0, p.S);
     } else {
 #pragma unroll
         for (int i = 0; i < NX; ++i) X[i] = 0.f;
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
             }
         }
     }
-    if (has_out && !issuer && ci == nchunk) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, d);
+    if (has_out && !issuer && ci == nchunk) store_x_out(X, pr.x_out + xo, pr.x_out_t, jr, c0, p.S);
     if (OUT) {  // rows past the sequence's end
         for (int x = tid; x < (t_end - n) * (d / 4); x += kTfThreads)
             *reinterpret_cast<uint4*>(pr.out + ((((size_t)b * p.T + t0 + n + x / (d / 4)) * p.H + h) * d + (x % (d / 4)) * 4) * 4) =

@@ -79,8 +79,13 @@ def _ops(D, T):
 
 def _on_tcgen05(dt, T, D):
     """Heads of whole 16-byte vectors, bfloat16 ones up to 128 channels, float32
-    ones of 33 to 64, of enough tokens."""
-    return D % 8 == 0 and T > (32 if D <= 32 else 16) if dt == "bf16" else D % 4 == 0 and 32 < D <= 64 and T > 96
+    ones of 33 to 64, of enough tokens; bfloat16 ones of other widths above 32
+    are spread to such for more tokens."""
+    if dt == "f32":
+        return D % 4 == 0 and 32 < D <= 64 and T > 96
+    if D % 8:
+        return D > 32 and T > (64 if D <= 64 else 32)
+    return T > (32 if D <= 32 else 16)
 
 
 class Problem:
@@ -162,6 +167,12 @@ CASES = [
     ("f32", 1, 1100, 2, 36, True, True, None),
     ("f32", 3, 200, 1, 60, False, True, [200, 0, 131]),
     ("f32", 1, 300, 2, 66, True, True, None),
+    ("bf16", 2, 300, 3, 5, True, True, [300, 77]),        # heads that are spread first
+    ("bf16", 1, 1300, 2, 45, True, True, None),
+    ("bf16", 3, 200, 2, 127, True, True, [200, 0, 131]),
+    ("bf16", 1, 1000, 1, 67, False, True, None),
+    ("f32", 1, 1100, 2, 37, True, True, None),
+    ("f32", 3, 150, 2, 63, False, True, [150, 0, 131]),
 ]
 
 
@@ -258,7 +269,8 @@ def test_heads_of_128(vk, B, T, H, lens):
 
 
 @pytest.mark.parametrize("dt,B,T,H,D", [("bf16", 30, 300, 3, 40), ("bf16", 2, 2100, 2, 16), ("bf16", 25, 200, 5, 96),
-                                        ("bf16", 1, 4200, 2, 88), ("f32", 40, 150, 4, 44), ("f32", 2, 1500, 2, 32)])
+                                        ("bf16", 1, 4200, 2, 88), ("bf16", 30, 150, 3, 33),
+                                        ("bf16", 3, 1500, 2, 125), ("f32", 40, 150, 4, 50), ("f32", 40, 150, 4, 44), ("f32", 2, 1500, 2, 32)])
 def test_padded_heads_and_their_neighbours(vk, dt, B, T, H, D):
     """Heads narrower than the tensor cores' tiles, several a CTA and cut: only
     their own channels are written, inside buffers whose rest keeps its values."""
