@@ -304,6 +304,45 @@ def test_states_between_vector_boundaries(vk, dt, D, T):
     p.check_bwd(p.bwd(vk))
 
 
+@pytest.mark.parametrize("dt,D", [("f32", 64), ("f32", 9), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, -2.0, 1e15])
+def test_scales(vk, dt, D, scale):
+    """A scale of nothing, of no size that a state could carry, negative, large:
+    the states do not depend on it."""
+    p = Problem(dt, 2, 200, 2, D, 24, lens=[200, 65], scale=scale)
+    out, last = p.fwd(vk)
+    want, S, mag, M = seq.decay_attn(p.qd, p.kd, p.vd, p.wd, p.H, p.scale, p.sd, p.lensd)
+    n = _ops(D, 200)
+    _check("state", last, S, M, "f32", n)
+    if abs(scale) != 1e-30:  # outputs below 1e-24 may lose bits
+        _check("out", out, want, mag, dt, n)
+        p.check_bwd(p.bwd(vk))
+    else:
+        assert np.isfinite(_np(out)).all()
+
+
+def test_two_streams_at_once(vk):
+    """Calls side by side on two streams, each with workspaces of its own."""
+    import torch
+    probs = [Problem("bf16", 1, 3000, 3, 64, 25), Problem("f32", 2, 900, 3, 64, 26), Problem("bf16", 1, 2000, 2, 128, 27),
+             Problem("bf16", 2, 700, 3, 45, 28)]
+    want = [(p.fwd(vk), p.bwd(vk)) for p in probs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in probs]
+    spaces = [[vk.decay_attn_workspace(p.B, p.T, p.H, p.D, p.q.dtype, backward=b) for b in (False, True)] for p in probs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        got = []
+        for p, s, (wf, wb) in zip(probs, streams, spaces):
+            with torch.cuda.stream(s):
+                got.append((p.fwd(vk, workspace=wf), p.bwd(vk, workspace=wb)))
+    torch.cuda.synchronize()
+    vk.device_status()
+    for (wf, wb), (gf, gb) in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip((*wf, *wb), (*gf, *gb)))
+
+
 def test_rows_and_states_far_apart(vk):
     """Rows whose offsets pass 32 bits, in elements, and a pool of states of
     more than 4 GiB."""

@@ -157,6 +157,10 @@ def test_workspace_sizes(lib):
     assert size(2, 100, 4, 64, 1, 0) == 0             # one segment: no cuts
     assert size(1, 100000, 1, 64, 1, 0) > 0
     assert size(1, 100000, 1, 64, 1, 1) > 0
+    # heads that are spread: copies of three inputs and an output, or of four and three
+    assert size(64, 200, 16, 45, 1, 0) == 4 * 64 * 200 * 16 * 48 * 2
+    assert size(64, 200, 16, 45, 1, 1) == 7 * 64 * 200 * 16 * 48 * 2
+    assert size(64, 200, 16, 45, 0, 0) == 0 and size(64, 60, 16, 45, 1, 0) == 0
     assert size(0, 100, 4, 64, 1, 0) == 0 and size(2, 100, 4, 129, 1, 0) == 0
     assert lib.vrwkv_layer_norm_bwd_workspace_bytes(10, 64, 1) >= 2 * 64 * 4
     assert lib.vrwkv_layer_norm_bwd_workspace_bytes(10, 8193, 1) == 0
