@@ -243,17 +243,22 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
         constexpr uint32_t kIdX = tc::idesc_bf16(128, D, false, false);
         constexpr uint32_t kIdP = tc::idesc_bf16(128, D, false, true);
         constexpr uint32_t kIdU = tc::idesc_bf16(128, D, true, true);
-        // the products of pieces: the first into an accumulator, the others into the next
-        constexpr int kPa[6] = {0, 0, 1, 1, 0, 2}, kPb[6] = {0, 1, 0, 1, 2, 0};
+        // hh and hm at once, B's pieces h and m side by side as are the two accumulators
+        constexpr uint32_t kIdA2 = tc::idesc_bf16(128, 256, false, false);
+        constexpr uint32_t kIdX2 = tc::idesc_bf16(128, 2 * D, false, false);
+        constexpr uint32_t kIdP2 = tc::idesc_bf16(128, 2 * D, false, true);
+        constexpr uint32_t kIdU2 = tc::idesc_bf16(128, 2 * D, true, true);
+        // the products of pieces: hh into an accumulator (and hm), the others into the next
+        constexpr int kPa[5] = {0, 1, 1, 0, 2}, kPb[5] = {0, 0, 1, 2, 0};
         const uint32_t sq = tc::smem_u32(S.q), sk = tc::smem_u32(S.k), sv = tc::smem_u32(S.v), sx = tc::smem_u32(S.x);
         bool issued = false;
         auto issue_u = [&]() {                          // U = v^T K'
 #pragma unroll
-            for (int i = 0; i < 6; ++i) {
+            for (int i = 0; i < 5; ++i) {
                 const uint64_t da = tc::sw128_desc(sv + kPa[i] * kTile, 0), db = tc::sw128_desc(sk + kPb[i] * kTile, kTile);
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k)
-                    tc::mma_ss(tmem + kColU + (i ? 64 : 0), da + 128 * k, db + 128 * k, kIdU, i > 1 || k > 0);
+                    tc::mma_ss(tmem + kColU + (i ? 64 : 0), da + 128 * k, db + 128 * k, i ? kIdU : kIdU2, i > 0 || k > 0);
             }
             tc::commit(&S.u);
         };
@@ -265,11 +270,11 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
             if (tc::elect_one()) {
                 if (OUT) {
 #pragma unroll
-                    for (int i = 0; i < 6; ++i) {       // A = q K'^T
+                    for (int i = 0; i < 5; ++i) {       // A = q K'^T
                         const uint64_t da = tc::sw128_desc(sq + kPa[i] * kTile, 16), db = tc::sw128_desc(sk + kPb[i] * kTile, 16);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            tc::mma_ss(tmem + (i ? 128 : 0), da + 2 * k, db + 2 * k, kIdA, i > 1 || k > 0);
+                            tc::mma_ss(tmem + (i ? 128 : 0), da + 2 * k, db + 2 * k, i ? kIdA : kIdA2, i > 0 || k > 0);
                     }
                     tc::commit(&S.a);
                 }
@@ -283,11 +288,11 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
                 if (OUT) {
                     if (with_x) {
 #pragma unroll
-                        for (int i = 0; i < 6; ++i) {   // O = q X
+                        for (int i = 0; i < 5; ++i) {   // O = q X
                             const uint64_t da = tc::sw128_desc(sq + kPa[i] * kTile, 16), db = tc::sw128_desc(sx + kPb[i] * 8192, 16);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                tc::mma_ss(tmem + kColO + (i ? 64 : 0), da + 2 * k, db + 2 * k, kIdX, i > 1 || k > 0);
+                                tc::mma_ss(tmem + kColO + (i ? 64 : 0), da + 2 * k, db + 2 * k, i ? kIdX : kIdX2, i > 0 || k > 0);
                         }
                         tc::commit(&S.qx);
                     }
@@ -307,12 +312,12 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
                 if (tc::elect_one()) {                  // O += P v
                     const uint32_t acc = with_x ? 1u : 0u;
 #pragma unroll
-                    for (int i = 0; i < 6; ++i) {
+                    for (int i = 0; i < 5; ++i) {
                         const uint64_t db = tc::sw128_desc(sv + kPb[i] * kTile, kTile);
 #pragma unroll
                         for (int k = 0; k < C / 16; ++k)
                             tc::mma_ts(tmem + kColO + (i ? 64 : 0), tmem + 64 * (k / 2) + 16 * kPa[i] + 8 * (k % 2), db + 128 * k,
-                                       kIdP, i > 1 || k > 0 ? 1u : acc);
+                                       i ? kIdP : kIdP2, i > 0 || k > 0 ? 1u : acc);
                     }
                     tc::commit(&S.o);
                 }
