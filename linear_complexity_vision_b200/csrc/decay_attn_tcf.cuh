@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
         for (int ci = 0; ci < nchunk; ++ci) {
             const bool more = ci + 1 < nchunk, update = more || has_out, with_x = ci > 0 || has_in;
             if (!wait(S.kt, ci)) break;
+            if (OUT && ci > 0 && !wait(S.o, ci - 1)) break;  // P, in A's columns, is read
             tc::fence_after();
             issued = true;
             if (tc::elect_one()) {
@@ -339,18 +340,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     for (; ci < nchunk && !issuer; ++ci) {
         const int a = first(ci), m = min(C, n - a);
         const bool more = ci + 1 < nchunk, update = more || has_out, with_x = OUT && (ci > 0 || has_in);
-        // the tiles' pieces
-        if (ci > 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (OUT) fetch(0, i, a, m, rq[i]);
-                fetch(1, i, a, m, rk[i]);
-            }
-            put_qk([&](int r) {
-                return fast ? S.col[r] : OUT ? 1.0f : S.pw[rev ? r + 1 : max(m - 1 - r, 0)] * pr.scale_upd;
-            });
-            arrive(S.kt);
-        }
+        // v's pieces; q's and k's were formed while the chunk before ended
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float rv[8];
@@ -359,6 +349,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
         }
         tc::fence_async_smem();
         arrive(S.kv);
+        if (more) prefetch(ci + 1, OUT ? 0 : 1);
         if (!OUT && !fast && update) arrive(S.kt2);     // K' was U's at once
         if (OUT) {
             if (!wait(S.a, ci)) break;
@@ -456,7 +447,6 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
             tc::fence_before();
             arrive(S.pr);
         }
-        if (more) prefetch(ci + 1, OUT ? 0 : 1);
         if (update) {
             if (!wait(S.u, ci)) break;
             tc::fence_after();
@@ -471,6 +461,18 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
                 store_x(min(C, n - first(ci + 1)));
                 tc::fence_async_smem();
                 arrive(S.xr);
+            }
+            if (more) {  // U was the last to read k, and followed O = q X: the next chunk's, while P v runs
+                const int a2 = first(ci + 1), m2 = min(C, n - a2);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (OUT) fetch(0, i, a2, m2, rq[i]);
+                    fetch(1, i, a2, m2, rk[i]);
+                }
+                put_qk([&](int r) {
+                    return fast ? S.col[r] : OUT ? 1.0f : S.pw[rev ? r + 1 : max(m2 - 1 - r, 0)] * pr.scale_upd;
+                });
+                arrive(S.kt);
             }
         }
         if (OUT) {
