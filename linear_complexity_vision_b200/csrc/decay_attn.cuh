@@ -528,7 +528,9 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepPara
     __shared__ float4 part[kStepRows / 4][kStepCols / 4];  // one row per warp
     const int b = blockIdx.x, h = blockIdx.y, slab = blockIdx.z, tid = threadIdx.x, D = p.D;
     const int c4 = tid % (kStepCols / 4), r0 = tid / (kStepCols / 4);
-    const int j = slab * kStepCols + 4 * c4;
+    // columns j, j + dj, ..: four in a row as a vector, else 8 apart, so that 8
+    // lanes read 8 in a row
+    const int dj = p.vec ? 1 : kStepCols / 4, j = slab * kStepCols + (p.vec ? 4 * c4 : c4);
     const int slot = p.slots ? __ldg(p.slots + b) : b;
     const bool in_range = slot >= 0 && slot < p.N;
     constexpr int es = sizeof(IO);
@@ -545,9 +547,9 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepPara
                 x[m] = __ldcs(reinterpret_cast<const float4*>(s));
             } else {
                 x[m].x = s[0];
-                if (j + 1 < D) x[m].y = s[1];
-                if (j + 2 < D) x[m].z = s[2];
-                if (j + 3 < D) x[m].w = s[3];
+                if (j + dj < D) x[m].y = s[dj];
+                if (j + 2 * dj < D) x[m].z = s[2 * dj];
+                if (j + 3 * dj < D) x[m].w = s[3 * dj];
             }
         }
     }
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepPara
     float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (j + e < D) v[e] = Io<IO>::ld1(p.v + ((size_t)b * p.ldv + (size_t)h * D + j + e) * es);
+        if (j + e * dj < D) v[e] = Io<IO>::ld1(p.v + ((size_t)b * p.ldv + (size_t)h * D + j + e * dj) * es);
     const float lam = decay_pow(__ldg(p.w + h), 1);
     // a slot that an earlier row names belongs to that row
     bool taken = false;
@@ -589,9 +591,9 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepPara
                     __stcs(reinterpret_cast<float4*>(s), x[m]);
                 } else {
                     s[0] = x[m].x;
-                    if (j + 1 < D) s[1] = x[m].y;
-                    if (j + 2 < D) s[2] = x[m].z;
-                    if (j + 3 < D) s[3] = x[m].w;
+                    if (j + dj < D) s[dj] = x[m].y;
+                    if (j + 2 * dj < D) s[2 * dj] = x[m].z;
+                    if (j + 3 * dj < D) s[3 * dj] = x[m].w;
                 }
             }
         }
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepPara
     if ((tid & 31) < kStepCols / 4) part[tid >> 5][c4] = o;
     __syncthreads();
     if (tid < kStepCols) {
-        const int jj = slab * kStepCols + tid;
+        const int jj = slab * kStepCols + (p.vec ? tid : tid / 4 + tid % 4 * (kStepCols / 4));
         float s = 0.f;
 #pragma unroll
         for (int q = 0; q < kStepRows / 4; ++q) s += reinterpret_cast<const float*>(&part[q][0])[tid];

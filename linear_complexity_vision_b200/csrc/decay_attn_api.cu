@@ -75,7 +75,7 @@ int padded_d(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 //                         outputs          states only      CTAs of an SM
 //   tcgen05, D <= 64      1.75             2.0 (+ 0.5)      1 (persistent), 2
 //            D <= 128     4.2              3.0              1
-//            float32      7.3              4.5              1
+//            float32      6.5              4.5              1
 //   any size, DP = 32     9 (+ 0.6)        4 (+ 0.6)        3
 //             DP = 64     23 (+ 0.6)       9 (+ 0.6)        3
 //             DP = 128    45               18               1
@@ -102,7 +102,7 @@ double pass_us(long long ctas, int units, const PassCost& c) {
 }
 
 Cut plan(int B, int T, int H, int D, vrwkv_dtype dtype, int nprob, bool tc) {
-    static const PassCost kOut[6] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}, {7.3, 0, 1}};
+    static const PassCost kOut[6] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}, {6.5, 0, 1}};
     static const PassCost kState[6] = {{2.0, 0.5, 2}, {3.0, 0, 1}, {4, 0.6, 3}, {9, 0.6, 3}, {18, 0, 1}, {4.5, 0, 1}};
     const int kind = tc ? (dtype == VRWKV_F32 ? 5 : D <= 64 ? 0 : 1) : (D <= 32 ? 2 : D <= 64 ? 3 : 4);
     const int units = (T + kSegUnit - 1) / kSegUnit;

@@ -26,19 +26,21 @@
 //
 // 16 working warps (a warp's number mod 4: its quarter of the rows; its
 // warpgroup: a block of P's columns, 16 columns of O, 16 of U) and one that
-// issues.  The next chunk's rows are brought to L2 as soon as P is done; the
+// issues.  The next chunk's rows are brought to L2 as soon as v is there; the
 // workers read, split and write them to shared memory in the swizzled layout (any
-// row stride that keeps 16-byte alignment), v behind A; the first chunk's q and
-// k are loaded and split while barriers, tables and tensor memory are set up.
+// row stride that keeps 16-byte alignment), v behind A; the next chunk's q and k
+// are split while P v runs, the first one's while barriers, tables and tensor
+// memory are set up.
 // 168 KB of shared memory, all of tensor memory, one CTA per SM.  Bounded waits
 // as in decay_attn_tc.cuh.
 //
-// Measured: 32 x 196 ragged, 6 heads: 35.5 us (floor 4.7: its bytes); backward 3
-// x 1001, 6 heads, eight segments: 50.4 us (3.7); the kernel for any size takes
-// 52 and 62 us.  A chunk takes 7.3 us, a CTA of one chunk 10 us: 144 products of
-// 64 to 128 columns, each fed from shared memory, are 4 us of that (the tensor
-// pipe is busy 13 % of the time), the splits into pieces 2 us, waits for one
-// another the rest.
+// Measured: 32 x 196 ragged, 6 heads: 33.5 us (floor 4.7: its bytes); backward 3
+// x 1001, 6 heads, eight segments: 50.2 us (3.7); the kernel for any size takes
+// 52 and 62 us.  A chunk takes 6.3 us, a CTA of one chunk 10 us.  The working
+// warps are busy 5.5 us of a chunk: splitting q, k and v 2.4 with their loads
+// from L2, P 1.4, X and the output 0.8; the products, fed from shared memory,
+// run beside that.  Loads begun earlier, and v's held in registers, spill (96 a
+// thread): 37.9 and 52.3 us.
 #pragma once
 
 #include "decay_attn_tc.cuh"
