@@ -381,7 +381,7 @@ def test_decays(vk, dt, D, w):
     p.check_bwd(p.bwd(vk))
 
 
-@pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 24)])
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 24), ("bf16", 45), ("f32", 44)])
 def test_rows_past_the_end_are_not_used(vk, dt, D):
     """NaN and infinities behind the sequences' ends change no bit."""
     import torch
@@ -564,6 +564,7 @@ def test_streams_graphs_and_workspaces(vk):
     import torch
     p = Problem("bf16", 1, 1500, 2, 64, 11)
     f = Problem("f32", 2, 300, 2, 48, 12, lens=[300, 100])
+    odd = Problem("bf16", 2, 1300, 2, 61, 29, lens=[1300, 700])
     gamma, beta = torch.ones(128, device="cuda"), torch.zeros(128, device="cuda")
 
     def calls(p):
@@ -583,7 +584,7 @@ def test_streams_graphs_and_workspaces(vk):
             return [out, last, *grads, y, mean, rstd, *ln, o, pool]
         return run
 
-    for prob in (p, f):
+    for prob in (p, f, odd):
         want = [t.clone() for t in calls(prob)()]
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
