@@ -473,12 +473,10 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  * Arithmetic: sums, decays and states in float32, products on the tensor
  *   cores from operands split into parts; outputs rounded once.
  *   float32    what the parts leave out is below 2^-21 of a product.
- *   bfloat16   q, k, v (gy) as they are; a state that meets q in two bfloat16
- *              parts (2^-17), one that leaves the call formed from three
- *              (2^-24).  The decayed products q.k and the decayed keys that
- *              meet v are in two parts too; calls of B*T*H >= 8192 may round
- *              them to one bfloat16: in outputs these roundings, half a step each
- *              and independent, weigh as much as the final one.
+ *   bfloat16   q, k, v (gy) as they are; a state that meets q, the decayed
+ *              products q.k and the decayed keys that meet v in two bfloat16
+ *              parts (2^-17); a state that leaves the call formed from three
+ *              (2^-24).
  *   Heads of a multiple of 8 channels (float32: 36 to 64, a multiple of 4;
  *   bfloat16 above 32: any) in tensors whose rows, outputs and states are
  *   16-byte aligned take the fifth-generation tensor cores from 17 to 97

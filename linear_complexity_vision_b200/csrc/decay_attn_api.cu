@@ -224,25 +224,25 @@ bool encode_tokens(CUtensorMap* m, const void* x, long long ld, int B, int T, in
 // Rows that start on 16-byte boundaries (and a stride that TMA can hold).
 bool rows16(const void* x, long long ld, int es) { return aligned(x, 16) && ld * es % 16 == 0 && ld < (1LL << 36); }
 
-template <int D, bool OUT, int PIECES, int PP, bool PAD>
+template <int D, bool OUT, int PIECES, bool PAD>
 vrwkv_status launch_tc_pad(const decay::TcParams& p, unsigned ctas, bool follows, cudaStream_t s) {
     static SmemGrants granted;
     constexpr int smem = decay::tc_smem_bytes<D, OUT>();
-    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT, PIECES, PP, PAD>, granted, smem);
+    const cudaError_t e = ensure_smem(decay::decay_attn_tc_kernel<D, OUT, PIECES, PAD>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    return launch(decay::decay_attn_tc_kernel<D, OUT, PIECES, PP, PAD>, "decay_attn_tc_kernel launch", dim3(ctas),
+    return launch(decay::decay_attn_tc_kernel<D, OUT, PIECES, PAD>, "decay_attn_tc_kernel launch", dim3(ctas),
                   decay::tc_threads<D>(), smem, follows, s, p);
 }
-template <int D, bool OUT, int PIECES, int PP>
+template <int D, bool OUT, int PIECES>
 vrwkv_status launch_tc(const decay::TcParams& p, unsigned ctas, bool follows, cudaStream_t s) {
-    return OUT && p.p.D == D && p.p.S == D ? launch_tc_pad<D, OUT, PIECES, PP, !OUT>(p, ctas, follows, s)
-                             : launch_tc_pad<D, OUT, PIECES, PP, true>(p, ctas, follows, s);
+    return OUT && p.p.D == D && p.p.S == D ? launch_tc_pad<D, OUT, PIECES, !OUT>(p, ctas, follows, s)
+                             : launch_tc_pad<D, OUT, PIECES, true>(p, ctas, follows, s);
 }
-template <int PIECES, int PP>
+template <int PIECES>
 vrwkv_status launch_tc64(decay::TcParams& p, bool follows, cudaStream_t s) {
     static SmemGrants granted;
     constexpr int smem = decay::t64_smem_bytes();
-    const cudaError_t e = ensure_smem(decay::decay_attn_tc64_kernel<PIECES, PP>, granted, smem);
+    const cudaError_t e = ensure_smem(decay::decay_attn_tc64_kernel<PIECES>, granted, smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
     const unsigned ctas = (unsigned)std::min(p.nitems, sm_count());
     int left = (int)ctas;
@@ -252,7 +252,7 @@ vrwkv_status launch_tc64(decay::TcParams& p, bool follows, cudaStream_t s) {
         left /= radix[i];
     }
     p.step[3] = left;
-    return launch(decay::decay_attn_tc64_kernel<PIECES, PP>, "decay_attn_tc64_kernel launch", dim3(ctas),
+    return launch(decay::decay_attn_tc64_kernel<PIECES>, "decay_attn_tc64_kernel launch", dim3(ctas),
                   decay::kT64Threads, smem, follows, s, p);
 }
 template <bool OUT>
@@ -265,26 +265,12 @@ vrwkv_status launch_tcf(const decay::TcParams& p, bool follows, cudaStream_t s) 
                   decay::kTfThreads, smem, follows, s, p);
 }
 
-// Operands of the tensor cores as one bfloat16 each (P, K~) from this many
-// (sequence, token, head) rows on.  Their roundings, half a step each and
-// independent, then add to the output's own in quadrature: 1.41 times the
-// error of the rounded output (measured 1.41 to 1.42).  Over few rows a single
-// product's rounding could stand out, and time is latency: two pieces, 1.00.
-constexpr long long kRoundedRows = 8192;
-
 vrwkv_status launch_tc_any(decay::TcParams& p, bool exact, bool follows, cudaStream_t s) {
     const unsigned n = (unsigned)p.nitems;
-    const bool rounded = (long long)p.p.B * p.p.T * p.p.H >= kRoundedRows;
-    if (p.p.pr[0].out && p.p.D <= 64) {
-        if (rounded) return exact ? launch_tc64<3, 1>(p, follows, s) : launch_tc64<1, 1>(p, follows, s);
-        return exact ? launch_tc64<3, 2>(p, follows, s) : launch_tc64<2, 2>(p, follows, s);
-    }
-    if (p.p.pr[0].out) {
-        if (rounded) return exact ? launch_tc<128, true, 3, 1>(p, n, follows, s) : launch_tc<128, true, 1, 1>(p, n, follows, s);
-        return exact ? launch_tc<128, true, 3, 2>(p, n, follows, s) : launch_tc<128, true, 2, 2>(p, n, follows, s);
-    }
-    if (p.p.D <= 64) return exact ? launch_tc<64, false, 3, 2>(p, n, follows, s) : launch_tc<64, false, 2, 2>(p, n, follows, s);
-    return exact ? launch_tc<128, false, 3, 2>(p, n, follows, s) : launch_tc<128, false, 2, 2>(p, n, follows, s);
+    if (p.p.pr[0].out && p.p.D <= 64) return exact ? launch_tc64<3>(p, follows, s) : launch_tc64<2>(p, follows, s);
+    if (p.p.pr[0].out) return exact ? launch_tc<128, true, 3>(p, n, follows, s) : launch_tc<128, true, 2>(p, n, follows, s);
+    if (p.p.D <= 64) return exact ? launch_tc<64, false, 3>(p, n, follows, s) : launch_tc<64, false, 2>(p, n, follows, s);
+    return exact ? launch_tc<128, false, 3>(p, n, follows, s) : launch_tc<128, false, 2>(p, n, follows, s);
 }
 
 // Launch p's problems; with `tc`, on the tensor cores with its maps.

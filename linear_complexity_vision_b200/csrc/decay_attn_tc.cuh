@@ -14,10 +14,11 @@
 //   U  = v^T K~                       K~ = e^{-w (..)} k as bfloat16 pieces
 //   X^T = e^{-w n} X^T + U            in registers
 // X ends in bfloat16 outputs and is split in two, off by at most 2^-17 (half a
-// step of a remainder below 2^-8).  P and K~ are split so too (PP, PIECES = 2)
-// or, on larger problems, rounded to one bfloat16 (1); a state that leaves the
-// call (PIECES = 3) is formed from three pieces, which hold a float32 value
-// exactly.
+// step of a remainder below 2^-8).  P and K~ are split so too (PIECES = 2); a
+// state that leaves the call (PIECES = 3) is formed from three pieces, which
+// hold a float32 value exactly.  (P and K~ as one bfloat16 each: 8 x 4096, 16
+// heads of 64 in 70 us in place of 87, outputs 1.41 times as far from the exact
+// ones as their own rounding leaves them.)
 //
 // Decays.  Where |w| <= 1/2, e^{-w (t - s)} = e^{-w (t - 63)} e^{-w (63 - s)}
 // stays within e^{+-32}: P takes the column's factor alone, the row's factor
@@ -120,9 +121,8 @@ __device__ __forceinline__ uint32_t split_bf16(float2& x) {
 
 // One 32 x 32 block of P, in the columns at taddr that hold the same block of A:
 // the thread's row (lane, in a quarter of the chunk's rows), columns 32 j .., d4
-// blocks back in (walked) time.  Two pieces: 16 columns of A become 8 of hi and 8
-// of lo; one: 32 become 16.  pw, col, row: the tables of TcSmem.
-template <int PP>
+// blocks back in (walked) time.  16 columns of A become 8 of hi and 8 of lo.
+// pw, col, row: the tables of TcSmem.
 __device__ __forceinline__ void p_block(uint32_t taddr, int j, int d4, bool fast, int rev, int lane, int m,
                                         const float* pw, const float* col, const float* row) {
     float all[32];
@@ -130,7 +130,6 @@ __device__ __forceinline__ void p_block(uint32_t taddr, int j, int d4, bool fast
     const float2 f = f2(fast ? 1.0f : pw[d4 == 0 ? 0 : rev ? 32 * d4 - lane : 32 * d4 - 31 + lane]);
     const float* dg = row + 31 - lane;
     const float* cl = fast ? col + 32 * j : col;
-    [[maybe_unused]] uint32_t packed[16];
 #pragma unroll
     for (int g = 0; g < 32; g += 16) {
         float v[16];
@@ -154,7 +153,7 @@ __device__ __forceinline__ void p_block(uint32_t taddr, int j, int d4, bool fast
                 v[i + 2] = y.x;
                 v[i + 3] = y.y;
             }
-            if (d4 == 0 && PP == 2) {
+            if (d4 == 0) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (rev ? g + i < lane : g + i > lane) v[i] = 0.f;
@@ -165,29 +164,14 @@ __device__ __forceinline__ void p_block(uint32_t taddr, int j, int d4, bool fast
             for (int i = 0; i < 16; ++i)
                 if (32 * j + g + i >= m) v[i] = 0.f;
         }
-        if constexpr (PP == 2) {
-            uint32_t out[16];
+        uint32_t out[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float2 x = f2(v[2 * i], v[2 * i + 1]);
-                out[i] = split_bf16(x);
-                out[8 + i] = pack_bf16(x);
-            }
-            tc::tmem_st16(taddr + g, out);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) packed[g / 2 + i] = pack_bf16(f2(v[2 * i], v[2 * i + 1]));
+        for (int i = 0; i < 8; ++i) {
+            float2 x = f2(v[2 * i], v[2 * i + 1]);
+            out[i] = split_bf16(x);
+            out[8 + i] = pack_bf16(x);
         }
-    }
-    if constexpr (PP == 1) {
-        if (d4 == 0 && fast) {      // bits of the columns in the row's future
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int past = rev ? 2 * i + 1 - lane : lane - 2 * i;  // >= 1: both stay, 0: the nearer
-                packed[i] &= past > 0 ? 0xffffffffu : past < 0 ? 0u : rev ? 0xffff0000u : 0x0000ffffu;
-            }
-        }
-        tc::tmem_st16(taddr, packed);
+        tc::tmem_st16(taddr + g, out);
     }
 }
 
@@ -229,7 +213,7 @@ __device__ __forceinline__ void st_global_32(char* p, const uint32_t (&r)[8]) {
 
 // PAD: heads may be narrower than D.  (With the width a variable in every
 // launch, B = 1, T = 16384, 8 heads of 128 took 87 us in place of 80.)
-template <int D, bool OUT, int PIECES, int PP, bool PAD>
+template <int D, bool OUT, int PIECES, bool PAD>
 __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     decay_attn_tc_kernel(const __grid_constant__ TcParams P) {
     static_assert(D == 128 || !OUT, "outputs of D = 64 have a kernel of their own");
@@ -448,9 +432,8 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
 #pragma unroll
-                        for (int half = 0; half < PP; ++half)
-                            tc::mma_ts(tmem + kColO, tmem + (PP == 2 ? 16 * k + 8 * half : 32 * (k / 2) + 8 * (k % 2)),
-                                       db + 128 * k, kIdP, k + half > 0 ? 1u : acc);
+                        for (int half = 0; half < 2; ++half)
+                            tc::mma_ts(tmem + kColO, tmem + 16 * k + 8 * half, db + 128 * k, kIdP, k + half > 0 ? 1u : acc);
                     tc::commit(&S.o);
                 }
                 __syncwarp();
@@ -525,12 +508,12 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
                     if (PIECES == 3) {
                         mi[e] = split_bf16(y);
                         lo[e] = pack_bf16(y);
-                    } else if (PIECES == 2) {
+                    } else {
                         mi[e] = pack_bf16(y);
                     }
                 }
                 *reinterpret_cast<uint4*>(S.kh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if (PIECES >= 2) *reinterpret_cast<uint4*>(S.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                *reinterpret_cast<uint4*>(S.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
                 if (PIECES == 3) *reinterpret_cast<uint4*>(third + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
@@ -541,8 +524,8 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
             tc::fence_after();
             // P: the quarter's rows, the block wg blocks back in (walked) time
             const int j = rev ? (quad + wg) & 3 : (quad - wg) & 3;
-            if (wg > wq || 32 * j >= m) tc::tmem_zero<16 * PP>(lanes + 32 * j);  // before the sequence's start, or past the chunk's end
-            else p_block<PP>(lanes + 32 * j, j, wg, fast, rev, lane, m, S.pw, S.col, S.row);
+            if (wg > wq || 32 * j >= m) tc::tmem_zero<32>(lanes + 32 * j);  // before the sequence's start, or past the chunk's end
+            else p_block(lanes + 32 * j, j, wg, fast, rev, lane, m, S.pw, S.col, S.row);
             if (!fast && with_x) {
                 const int row = quad * 32 + lane;
                 const float2 f = f2(S.pw[max(rev ? m - 1 - row : row, 0) + e0] * pr.scale_inter);

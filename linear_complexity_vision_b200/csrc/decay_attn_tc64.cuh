@@ -45,7 +45,7 @@ struct alignas(1024) T64Smem {
         uint8_t q[16384], k[16384], v[16384], kh[16384], km[16384];
         uint8_t out[16384];          // the rows of O on their way out
     } st[2];
-    uint8_t x[16384];                // X^T as operands of the next chunk, hi and lo; with one piece of K~ km of its stream
+    uint8_t x[16384];                // X^T as operands of the next chunk, hi and lo
     Tables tab[2][2];                // [stream][item's turn]
     struct Bars {
         unsigned long long fa, fv, a, kt, u, pr, o, xr, of, uf, tb, qs, so, qk, drain;
@@ -131,7 +131,7 @@ struct T64Cursor {
     __device__ __forceinline__ bool with_x() const { return ci > 0 || it.has_in; }
 };
 
-template <int PIECES, int PP>
+template <int PIECES>
 __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const __grid_constant__ TcParams P) {
     constexpr int C = kTcChunk, D = 64;
     extern __shared__ __align__(1024) char smem_raw[];
@@ -247,12 +247,12 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                         if (PIECES == 3) {
                             mi[e] = split_bf16(y);
                             lo[e] = pack_bf16(y);
-                        } else if (PIECES == 2) {
+                        } else {
                             mi[e] = pack_bf16(y);
                         }
                     }
                     *reinterpret_cast<uint4*>(T.kh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if (PIECES >= 2) *reinterpret_cast<uint4*>(T.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                    *reinterpret_cast<uint4*>(T.km + off) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
                     if (PIECES == 3) *reinterpret_cast<uint4*>(T.k + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
@@ -267,10 +267,10 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                 const int d4 = wg == 0 ? 3 * jj : 1 + jj;
                 const int j = rev ? (quad + d4) & 3 : (quad - d4) & 3;
                 if (d4 > wq || 32 * j >= m) {           // before the sequence's start, or past the chunk's end
-                    tc::tmem_zero<16 * PP>(lanes + 32 * j);
+                    tc::tmem_zero<32>(lanes + 32 * j);
                     continue;
                 }
-                p_block<PP>(lanes + 32 * j, j, d4, fast, rev, lane, m, N.pw, N.col, N.row);
+                p_block(lanes + 32 * j, j, d4, fast, rev, lane, m, N.pw, N.col, N.row);
             }
             const int row = quad * 32 + lane;
             if (!fast && cu.with_x()) {
@@ -365,9 +365,8 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
                         hi[e] = split_bf16(x);
                         lo[e] = pack_bf16(x);
                     }
-                    uint8_t* xo = PIECES == 1 ? S.st[stream].km : S.x;
-                    *reinterpret_cast<uint4*>(xo + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(xo + 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4*>(S.x + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(S.x + 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 tc::fence_async_smem();
                 arrive(S.bar[stream].xr);
@@ -375,10 +374,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
             // after the last O = q X has read the buffer (a barrier of its own: a
             // may be a chunk without X ahead)
             auto next_x = [&](int m, int stream) {
-                const int from = PIECES == 1 ? stream : last;
-                if (stored[stream] + stored[stream ^ 1] > 0 && (PIECES > 1 || stored[stream] > 0) &&
-                    !wait(S.bar[from].qs, stored[from] - 1))
-                    return false;
+                if (stored[0] + stored[1] > 0 && !wait(S.bar[last].qs, stored[last] - 1)) return false;
                 store_x(m, stream);
                 ++stored[stream];
                 last = stream;
@@ -424,7 +420,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         constexpr uint32_t kIdU = tc::idesc_bf16(128, D, true, true);
         const uint32_t sq = tc::smem_u32(T.q), sk = tc::smem_u32(T.k), sv = tc::smem_u32(T.v);
         const uint32_t skh = tc::smem_u32(T.kh), skm = tc::smem_u32(T.km);
-        const uint32_t sxh = PIECES == 1 ? skm : tc::smem_u32(S.x), sxl = sxh + 8192, sout = tc::smem_u32(T.out);
+        const uint32_t sxh = tc::smem_u32(S.x), sxl = sxh + 8192, sout = tc::smem_u32(T.out);
         auto load = [&](uint32_t dst, int map, const T64Cursor& c, unsigned long long* bar) {
             tc::tma_load_4d(dst, &P.map[map], 0, c.it.h, c.it.t0 + c.first(), c.it.b, bar);
         };
@@ -546,9 +542,8 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k)
 #pragma unroll
-                    for (int half = 0; half < PP; ++half)
-                        tc::mma_ts(tmem + 128, tmem + (PP == 2 ? 16 * k + 8 * half : 32 * (k / 2) + 8 * (k % 2)),
-                                   db + 128 * k, kIdP, k + half > 0 ? 1u : acc);
+                    for (int half = 0; half < 2; ++half)
+                        tc::mma_ts(tmem + 128, tmem + 16 * k + 8 * half, db + 128 * k, kIdP, k + half > 0 ? 1u : acc);
                 tc::tma_store_wait(false);              // the output tile is free
                 tc::commit(&B.o);
             }
