@@ -485,8 +485,10 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  *   outputs of magnitudes from 1e-24 to 1e24.
  *   The same call on the same alignments gives the same bits; a sequence's
  *   bits may differ between batches of other sizes.
- *   Infinities and NaN among the valid tokens may also reach outputs of
- *   earlier tokens of the same 128-token block, as NaN.
+ *   Infinities and NaN among the valid tokens and in states reach every
+ *   result whose terms they are in, infinities as themselves or as NaN.  They
+ *   may also reach outputs of earlier tokens of the same 128-token block, as
+ *   NaN.
  */
 
 size_t vrwkv_decay_attn_workspace_bytes(int B, int T, int H, int D,

@@ -130,16 +130,21 @@ struct Cfg {
     static constexpr int kResident = DP == 128 ? 1 : 3;     // CTAs of an SM, by registers
 };
 
-// A float32 operand as tf32 values: hi to nearest, lo the remainder (of which
-// the tensor core reads the upper bits, so half a step is added first).
+// A float32 operand as tf32 values, of which the tensor core reads the upper 19
+// bits: hi, then lo, the remainder.  Cutting bits off a value times 1 + 2^-11
+// leaves it off by at most 2^-11 of itself either way, so hi + lo is off by 2^-22.
+// Float multiplications, since they keep a NaN (the GPU's own has all bits set:
+// adding to them wraps it to 0), and towards zero, since a finite value then
+// stays finite.  What an infinity leaves is NaN.
 template <bool EXACT>
 __device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) {
+    constexpr float kHalfStep = 1.00048828125f;
     if (EXACT) {
         hi = __float_as_uint(x);
         lo = 0u;
     } else {
-        hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-        lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+        hi = __float_as_uint(__fmul_rz(x, kHalfStep)) & 0xffffe000u;
+        lo = __float_as_uint((x - __uint_as_float(hi)) * kHalfStep);
     }
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

@@ -1,4 +1,5 @@
-"""What decay attention does to numbers: how often it rounds.
+"""What decay attention does to numbers: how often it rounds, and where NaN,
+infinities and values at the ends of the range go.
 
 Against the float64 oracle, with the names of test_gpu_sequence.py: u = 2^-24,
 n operations, A the sum of the absolute values of a result's terms.
@@ -60,3 +61,101 @@ def test_products_are_not_rounded_where_decays_are_factored(vk, B, T, H, D):  # 
     want, _, mag, _ = seq.decay_attn(p.qd, p.kd, p.vd, p.wd, H, p.scale)
     for state in (True, False):
         _rounded_once(p.fwd(vk, want_state=state)[0], want, mag, _ops(D, T))
+
+
+NAN, GPU_NAN, INF = 0x7fc00000, 0x7fffffff, 0x7f800000  # float32 bits; arithmetic on the GPU gives the second
+
+
+def _value(bits, dt):
+    """A value of these bits (their upper half in bfloat16)."""
+    import torch
+    t = torch.tensor([bits if dt == "f32" else bits >> 16], device="cuda")
+    return t.to(torch.int32).view(torch.float32) if dt == "f32" else t.to(torch.int16).view(torch.bfloat16)
+
+
+KERNELS = [("f32", 9, 200), ("f32", 64, 33), ("f32", 128, 150), ("bf16", 20, 150), ("bf16", 64, 16),  # any size
+           ("f32", 64, 300), ("bf16", 64, 300), ("bf16", 128, 300), ("bf16", 45, 300),               # tcgen05
+           ("f32", 128, 2000), ("bf16", 20, 2000), ("f32", 64, 2000), ("bf16", 64, 2000), ("bf16", 128, 2000)]  # cut
+
+
+def _all_bad(t):
+    import torch
+    return not torch.isfinite(t).any()
+
+
+@pytest.mark.parametrize("bits", [NAN, GPU_NAN, INF])
+@pytest.mark.parametrize("dt,D,T", KERNELS)
+def test_what_is_not_finite_stays_so(vk, dt, D, T, bits):  # noqa: F811
+    """One NaN or infinity among the valid tokens.  With w = 0.01, no term decays to 0
+    and no value is 0, so it reaches all that the recurrence leads it to.  In q it
+    reaches its row of out and, through q^T g, the column it is in of G_t, t <= its
+    own, and so on."""
+    import torch
+    at, c = T // 2, D + 2                                # a token, and a channel: head 1, its channel 2
+    for name in "qkvg":
+        p = Problem(dt, 1, T, 2, D, 33, w=0.01)
+        clean_out, clean_last = p.fwd(vk)
+        getattr(p, name)[0, at, c] = _value(bits, dt)
+        out, last = (t.clone() for t in p.fwd(vk))
+        gq, gk, gv, gs = p.bwd(vk)
+        o, grads = out[0].view(T, 2, D), [t[0].view(T, 2, D) for t in (gq, gk, gv)]
+        assert torch.equal(o[:, 0], clean_out[0].view(T, 2, D)[:, 0])  # the other head does not see it
+        for t in grads:
+            assert torch.isfinite(t[:, 0]).all()
+        if name == "q":                                  # out_t = q_t S_t; G_s = .. + q_t^T g_t for s <= t
+            assert _all_bad(o[at, 1]) and torch.isfinite(o[at + 1:, 1]).all() and torch.isfinite(last).all()
+            assert _all_bad(gs[0, 1, 2]) and _all_bad(grads[1][:at + 1, 1, 2]) and _all_bad(grads[2][:at + 1, 1])
+        if name == "k":                                  # row 2 of S_t, t >= its own
+            assert _all_bad(o[at:, 1]) and _all_bad(last[0, 1, 2])
+            assert _all_bad(grads[0][at:, 1, 2]) and _all_bad(grads[2][at, 1])
+        if name == "v":                                  # column 2 of S_t, t >= its own
+            assert _all_bad(o[at:, 1, 2]) and _all_bad(last[0, 1, :, 2])
+            assert _all_bad(grads[0][at:, 1]) and _all_bad(grads[1][at, 1])
+        if name == "g":                                  # column 2 of G_t, t <= its own
+            assert _all_bad(grads[0][at, 1]) and _all_bad(gs[0, 1, :, 2])
+            assert _all_bad(grads[1][:at + 1, 1]) and _all_bad(grads[2][:at + 1, 1, 2])
+    vk.device_status()
+
+
+@pytest.mark.parametrize("bits", [NAN, GPU_NAN, INF])
+@pytest.mark.parametrize("dt,D,T", KERNELS)
+def test_states_and_decays_that_are_not_finite(vk, dt, D, T, bits):  # noqa: F811
+    """One in the state before the first token, in the gradient of the one after the
+    last, and a decay that is NaN."""
+    import torch
+    p = Problem(dt, 1, T, 2, D, 34, w=0.01)
+    p.s[0, 1, 3, 2] = _value(bits, "f32")
+    out, last = p.fwd(vk)
+    assert _all_bad(out[0].view(T, 2, D)[:, 1, 2]) and not torch.isfinite(last[0, 1, 3, 2])
+    assert torch.isfinite(out[0].view(T, 2, D)[:, 0]).all() and torch.isfinite(last[0, 0]).all()
+    assert _all_bad(p.bwd(vk)[0][0].view(T, 2, D)[:, 1, 3])
+    p = Problem(dt, 1, T, 2, D, 35, w=0.01)
+    p.gs[0, 1, 3, 2] = _value(bits, "f32")
+    gq, gk, gv, gs = (None if t is None else t[0] for t in p.bwd(vk))
+    assert _all_bad(gk.view(T, 2, D)[:, 1, 3]) and _all_bad(gv.view(T, 2, D)[:, 1, 2]) and not torch.isfinite(gs[1, 3, 2])
+    assert torch.isfinite(gq).all() and all(torch.isfinite(t.view(T, 2, D)[:, 0]).all() for t in (gk, gv))
+    if bits != INF:
+        p = Problem(dt, 1, T, 2, D, 36)
+        p.w[1] = _value(bits, "f32")
+        out, last = p.fwd(vk)
+        grads = p.bwd(vk)
+        # (gk and gv of the last token and, without a state, gq and out of the first hold no decay)
+        assert _all_bad(out[0].view(T, 2, D)[:, 1]) and _all_bad(last[0, 1]) and _all_bad(grads[3][0, 1])
+        assert all(_all_bad(t[0].view(T, 2, D)[1:-1, 1]) for t in grads[:3])
+        assert torch.isfinite(out[0].view(T, 2, D)[:, 0]).all()
+    vk.device_status()
+
+
+@pytest.mark.parametrize("D,T", [(9, 100), (64, 64), (128, 200)])
+def test_largest_float32_values(vk, D, T):  # noqa: F811
+    """Values up to the type's largest, in v, where the state and the result are far
+    below it.  Parts: 3 * 2^-22 of a product of float32 values, twice in a row."""
+    p = Problem("f32", 1, T, 1, D, 37, state=False, w=3.0, scale=2.0 ** -60)
+    p.v[0, ::3, ::2] = float(np.finfo(np.float32).max)
+    p.vd = _np(p.v)
+    p.k *= 2.0 ** -30                                    # the state holds sums of k v
+    p.kd = _np(p.k)
+    out = p.fwd(vk, want_state=False)[0]
+    assert vk.load_library().vrwkv_last_kernel() == b"decay_attn_kernel"
+    want, _, mag, _ = seq.decay_attn(p.qd, p.kd, p.vd, p.wd, 1, p.scale)
+    assert (np.abs(_np(out) - want) <= (_ops(D, T) * U + 2.0 ** -19) * mag).all()
