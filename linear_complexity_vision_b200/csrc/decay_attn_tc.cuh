@@ -112,9 +112,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float2 x) {
 __device__ __forceinline__ float2 unpack_bf16(uint32_t h) {
     return f2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u));
 }
-// x rounded to bfloat16 (returned); x becomes what the rounding left out.
+// x rounded to bfloat16 (returned), at most to the largest finite value: x becomes
+// what the rounding left out, and the last piece, not bounded, keeps an infinity.
 __device__ __forceinline__ uint32_t split_bf16(float2& x) {
-    const uint32_t h = pack_bf16(x);
+    uint32_t h;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x.y), "f"(x.x));
     x = fma2(unpack_bf16(h), f2(-1.0f), x);
     return h;
 }

@@ -159,3 +159,22 @@ def test_largest_float32_values(vk, D, T):  # noqa: F811
     assert vk.load_library().vrwkv_last_kernel() == b"decay_attn_kernel"
     want, _, mag, _ = seq.decay_attn(p.qd, p.kd, p.vd, p.wd, 1, p.scale)
     assert (np.abs(_np(out) - want) <= (_ops(D, T) * U + 2.0 ** -19) * mag).all()
+
+
+def test_largest_float32_values_in_three_parts(vk):  # noqa: F811
+    """The same on the fifth-generation tensor cores.  Values above 3.3962e38 are
+    nearer to 2^128 than to bfloat16's largest, which the first part of three then
+    is.  What the parts leave out: 2^-23 of a product, twice in a row."""
+    for w in (3.0, 0.2):
+        p = Problem("f32", 1, 300, 2, 64, 38, state=False, w=w, scale=2.0 ** -20)
+        p.v[0, ::3, ::2] = float(np.finfo(np.float32).max)
+        p.vd = _np(p.v)
+        p.k *= 2.0 ** -60
+        p.kd = _np(p.k)
+        for keep in (True, False):
+            out, last = p.fwd(vk, want_state=keep)
+            assert vk.load_library().vrwkv_last_kernel() == b"decay_attn_tcf_kernel"
+            want, S, mag, M = seq.decay_attn(p.qd, p.kd, p.vd, p.wd, 2, p.scale)
+            tol = _ops(64, 300) * U + 2.0 ** -22
+            assert (np.abs(_np(out) - want) <= tol * mag).all()
+            assert last is None or (np.abs(_np(last) - S) <= tol * M).all()
