@@ -481,8 +481,8 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  *   bfloat16 above 32: any) in tensors whose rows, outputs and states are
  *   16-byte aligned take the fifth-generation tensor cores from 17 to 97
  *   tokens on (by type and D), the rest a kernel for any size.  On the
- *   former, where |w| <= 1/2, sums carry factors within e^+-32: safe for
- *   outputs of magnitudes from 1e-24 to 1e24.
+ *   former, where |w| <= 1/2 and |scale| lies from 1e-12 to 1e12, sums carry
+ *   factors within e^+-32: safe for outputs of magnitudes from 1e-24 to 1e24.
  *   The same call on the same alignments gives the same bits; a sequence's
  *   bits may differ between batches of other sizes.
  *   Infinities and NaN among the valid tokens and in states reach every

@@ -20,7 +20,7 @@
 // heads of 64 in 70 us in place of 87, outputs 1.41 times as far from the exact
 // ones as their own rounding leaves them.)
 //
-// Decays.  Where |w| <= 1/2, e^{-w (t - s)} = e^{-w (t - 63)} e^{-w (63 - s)}
+// Decays.  Where |w| <= 1/2 (and the scale is of a size to spare, factored()), e^{-w (t - s)} = e^{-w (t - 63)} e^{-w (63 - s)}
 // stays within e^{+-32}: P takes the column's factor alone, the row's factor
 // multiplies the finished row of O, and X enters times e^{-64 w}, so that
 // O = q X and O += P v add up without a pass between them.  (A sum may then
@@ -60,7 +60,6 @@ namespace vrwkv {
 namespace decay {
 
 constexpr int kTcChunk = 128;
-constexpr float kTcFastW = 0.5f;
 constexpr unsigned kTcErr = 8u;
 
 struct TcParams {
@@ -74,6 +73,14 @@ struct TcParams {
     unsigned int* err;
     unsigned long long wait_ns;
 };
+
+// Whether a problem's decays are taken as a column's factor times a row's, within
+// e^{+-32}.  The column's carries the scale: where that is tiny or huge, bits or
+// values would be lost between the two.
+__device__ __forceinline__ bool factored(float w, const Problem& pr) {
+    const float s = fabsf(pr.scale_intra);
+    return fabsf(w) <= 0.5f && s >= 1e-12f && s <= 1e12f;
+}
 
 template <int D>
 __host__ __device__ constexpr int tc_threads() {
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(tc_threads<D>(), D == 64 ? 2 : 1)
     }
     if (warp == 1) tc::tmem_alloc(&S.tmem, kCols);
     const DecayBase base = decay_base(w);
-    const bool fast = fabsf(w) <= kTcFastW;
+    const bool fast = factored(w, pr);
     for (int i = tid; i <= C; i += kThreads) S.pw[i] = decay_pow(base, i);
     if (OUT && tid < C) {
         if (fast) {

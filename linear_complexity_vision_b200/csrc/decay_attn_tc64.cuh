@@ -59,7 +59,7 @@ constexpr int t64_smem_bytes() { return (int)sizeof(T64Smem) + 1024; }
 // A work item: one head's segment of one problem.
 struct T64Item {
     int prob, seg, h, b;  // its number's digits, the problem fastest
-    int t0, n, nchunk, rev, has_in, has_out;
+    int t0, n, nchunk, rev, has_in, has_out, fast;
     float w;
     __device__ __forceinline__ void at(const TcParams& P, int item) {
         const Params& p = P.p;
@@ -91,13 +91,13 @@ struct T64Item {
         nchunk = (n + kTcChunk - 1) / kTcChunk;
         const Problem& pr = p.pr[prob];
         rev = pr.reverse;
+        fast = factored(w, pr);
         has_in = pr.x_in != nullptr;
         has_out = pr.x_out != nullptr;
     }
     __device__ __forceinline__ long long state_at(const Params& p) const {
         return (((long long)b * p.H + h) * p.nseg + seg) * p.S * p.S;
     }
-    __device__ __forceinline__ bool fast() const { return fabsf(w) <= kTcFastW; }
 };
 
 // A stream's walk over its chunks: every second one of the items' chunks in
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         for (int ph = 0; cu.valid(nitems); ++ph) {      // ph: chunks of this stream so far
             const T64Item& it = cu.it;
             const Problem& pr = p.pr[it.prob];
-            const bool fast = it.fast();
+            const bool fast = it.fast;
             const int rev = it.rev, m = cu.tokens();
             const bool update = cu.update();
             if (tables_of != cu.item) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
         for (int item = blockIdx.x; item < nitems && okay; item += gridDim.x, it.step(P)) {
             const Problem& pr = p.pr[it.prob];
             const DecayBase w = decay_base(it.w);
-            const bool fast = it.fast();
+            const bool fast = it.fast;
             const long long xo = it.state_at(p);
             float X[NX];
             if (it.has_in) {

@@ -85,8 +85,7 @@ __global__ void __launch_bounds__(kTfThreads, 1) decay_attn_tcf_kernel(const __g
     const bool issuer = warp == NW;
     const float w = __ldg(p.w + h);
     const DecayBase base = decay_base(w);
-    // K' carries the scale, which the state's update takes out again
-    const bool fast = fabsf(w) <= kTcFastW && fabsf(pr.scale_intra) >= 1e-12f && fabsf(pr.scale_intra) <= 1e12f;
+    const bool fast = factored(w, pr);           // K' carries the scale, which the state's update takes out again
     const int n_seq = seq_tokens(p.lengths, b, p.T);
     const int t0 = seg * p.seg_tokens;
     const int n = seg_count(n_seq, seg, p.seg_tokens);

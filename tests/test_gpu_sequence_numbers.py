@@ -178,3 +178,18 @@ def test_largest_float32_values_in_three_parts(vk):  # noqa: F811
             tol = _ops(64, 300) * U + 2.0 ** -22
             assert (np.abs(_np(out) - want) <= tol * mag).all()
             assert last is None or (np.abs(_np(last) - S) <= tol * M).all()
+
+
+@pytest.mark.parametrize("dt,D,T", [("bf16", 64, 200), ("bf16", 128, 200), ("bf16", 45, 200), ("bf16", 20, 200), ("f32", 64, 200),
+                                    ("f32", 9, 200), ("f32", 128, 100), ("bf16", 64, 2000), ("bf16", 128, 2000), ("f32", 64, 2000)])
+@pytest.mark.parametrize("scale", [1e-30, 1e-20, -1e-13, 1e20])
+def test_scales_of_any_size(vk, dt, D, T, scale):  # noqa: F811
+    """Outputs and gradients to the tolerances of ordinary scales.  Slow decays, so
+    that factors over a block of tokens lie far apart, and no gradient of the last
+    state, beside which G's other terms would not show.  At 1e-30 a part of 2^-24
+    of a term is above float32's smallest normal value 1.2e-38."""
+    p = Problem(dt, 2, T, 2, D, 39, lens=[T, T // 3], scale=scale, w=np.array([0.02, 0.45]))
+    p.gs = p.gsd = None
+    p.check_fwd(*p.fwd(vk))
+    p.check_bwd(p.bwd(vk))
+    vk.device_status()
