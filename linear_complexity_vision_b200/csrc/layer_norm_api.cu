@@ -53,6 +53,7 @@ LnBwdPlan ln_bwd_plan(long long rows, int C, int es, bool vec) {
     const int vectors = pl.vec ? C * es / 16 : C;
     if (pl.vec && (vectors + 31) / 32 * (16 / es) <= 32) {
         pl.vpl = (vectors + 31) / 32;
+        if (pl.vpl > 4) pl.vpl = (pl.vpl + 1) / 2 * 2;  // float32 alone: 6 or 8, the widths there are
         pl.threads = 32 * kLnBwdWarps;
         const int ctas = es == 4 ? ln_bwd_ctas<float>(pl.vpl) : ln_bwd_ctas<__nv_bfloat16>(pl.vpl);  // resident on an SM
         pl.grid = (int)std::min<long long>((rows + kLnBwdWarps - 1) / kLnBwdWarps, (long long)ctas * sm_count());
@@ -87,8 +88,8 @@ void launch_ln_bwd(const LayerNormBwdParams& p, const LnBwdPlan& pl, cudaStream_
     default: break;
     }
     if constexpr (sizeof(IO) == 4) {  // vectors of 4 channels: up to 8 a lane
-        if (pl.vpl == 5 || pl.vpl == 6) return launch_ln_bwd_warp<IO, 6>(p, pl, s);
-        if (pl.vpl > 6) return launch_ln_bwd_warp<IO, 8>(p, pl, s);
+        if (pl.vpl == 6) return launch_ln_bwd_warp<IO, 6>(p, pl, s);
+        if (pl.vpl == 8) return launch_ln_bwd_warp<IO, 8>(p, pl, s);
     }
     if (pl.vec) {
         if (pl.nv == 1) layer_norm_bwd_kernel<IO, true, 1><<<pl.grid, pl.threads, 0, s>>>(p);

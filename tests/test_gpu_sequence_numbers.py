@@ -7,6 +7,7 @@ n operations, A the sum of the absolute values of a result's terms.
 import numpy as np
 import pytest
 
+import test_gpu_sequence as base
 from oracle import sequence as seq
 from test_gpu_sequence import U, Problem, _dev, _np, _ops, vk  # noqa: F401
 
@@ -193,3 +194,10 @@ def test_scales_of_any_size(vk, dt, D, T, scale):  # noqa: F811
     p.check_fwd(*p.fwd(vk))
     p.check_bwd(p.bwd(vk))
     vk.device_status()
+
+
+@pytest.mark.parametrize("dt,rows,C", [("f32", 700, 516), ("f32", 1500, 640), ("f32", 50, 772), ("f32", 1300, 896), ("bf16", 1500, 640),
+                                       ("bf16", 700, 520)])
+def test_layer_norm_widths(vk, dt, rows, C):  # noqa: F811
+    """Rows narrower than the kernel they go to, more of them than CTAs."""
+    base.test_layer_norm(vk, dt, rows, C)

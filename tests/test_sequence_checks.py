@@ -166,6 +166,19 @@ def test_workspace_sizes(lib):
     assert lib.vrwkv_layer_norm_bwd_workspace_bytes(10, 8193, 1) == 0
 
 
+def test_layer_norm_bwd_partial_rows(lib):
+    """Widths that the same kernel serves get the same number of CTAs, each with a
+    partial row of 2 C floats: as many as stay on an SM at a time."""
+    rows = 1 << 20
+
+    def ctas(C):
+        n = lib.vrwkv_layer_norm_bwd_workspace_bytes(rows, C, 0)
+        return n // (8 * C)                              # bytes are rounded up to 256, less than a row
+    assert ctas(516) == ctas(640) == ctas(768)           # 6 vectors a lane
+    assert ctas(772) == ctas(896) == ctas(1024)          # 8
+    assert ctas(512) >= ctas(768) >= ctas(1024)
+
+
 # ---- the binding ----
 
 
