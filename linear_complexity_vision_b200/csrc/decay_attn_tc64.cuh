@@ -19,7 +19,8 @@
 //
 // Roles (704 threads): warps 0-7 and 8-15 the workers of streams 0 and 1,
 // warps 16-19 the state, warps 20-21 the issuers.  512 tensor-memory columns:
-// per stream A / P 128, O 64, U 64.  Bounded waits as in decay_attn_tc.cuh.
+// per stream A / P 128, O 64, U 64.  Bounded waits as in decay_attn_tc.cuh; here
+// only the state warps need the pass before, so a wait's time begins after it.
 //
 // A barrier is waited for by its phase's parity, so no phase may complete
 // before every waiter has seen the one before.  That holds because each phase
@@ -166,8 +167,11 @@ __global__ void __launch_bounds__(kT64Threads, 1) decay_attn_tc64_kernel(const _
     tc::fence_after();
     volatile int* abort = &S.abort;
     auto wait = [&](unsigned long long& bar, int phase) {  // the whole warp
-        const bool w = tc::mbar_test(&bar, (unsigned)phase & 1u) ||
-                       tc::wait_slow(&bar, (unsigned)phase & 1u, abort, P.err, kTcErr, P.wait_ns);
+        bool w = tc::mbar_test(&bar, (unsigned)phase & 1u);
+        if (!w) {
+            last_pass();  // what the pass before still takes is not counted
+            w = tc::wait_slow(&bar, (unsigned)phase & 1u, abort, P.err, kTcErr, P.wait_ns);
+        }
         return __all_sync(0xffffffffu, w ? 1 : 0) != 0;
     };
     auto arrive = [&](unsigned long long& bar) {

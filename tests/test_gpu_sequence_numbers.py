@@ -201,3 +201,24 @@ def test_scales_of_any_size(vk, dt, D, T, scale):  # noqa: F811
 def test_layer_norm_widths(vk, dt, rows, C):  # noqa: F811
     """Rows narrower than the kernel they go to, more of them than CTAs."""
     base.test_layer_norm(vk, dt, rows, C)
+
+
+def test_wait_limits_do_not_count_the_pass_before(vk):  # noqa: F811
+    """The states at the cuts take some hundred us on most SMs, while CTAs of the
+    outputs' pass are set up on the others: with a limit of 20 us for a wait, these
+    still report nothing and give the same bits."""
+    import torch
+    B, T, H, D = 1, 262144, 12, 64
+    torch.manual_seed(40)
+    q, k, v = (torch.randn(B, T, H * D, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    w = torch.full((H,), 0.01, device="cuda")
+    want = vk.decay_attn_fwd(q, k, v, w, H, D ** -0.5)
+    vk.device_status()
+    vk.set_wait_limit(2e-5)
+    try:
+        for _ in range(3):
+            got = vk.decay_attn_fwd(q, k, v, w, H, D ** -0.5)
+            vk.device_status()
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+    finally:
+        vk.set_wait_limit(2.0)
