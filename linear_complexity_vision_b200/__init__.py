@@ -477,6 +477,7 @@ def biwkv_bwd(k, v, w, u, gy, totals: bool = True, out=None):
 # directly, and what a size needs of workspace is remembered by the size.
 _torch = None
 _ws_need = {}
+_WS_NEED_MOST = 4096  # sizes remembered at a time
 
 
 def _load_torch():
@@ -576,6 +577,8 @@ def _workspace(key, size, workspace, device, f32):
     key = (device.index, *key)
     need = _ws_need.get(key)
     if need is None:
+        if len(_ws_need) >= _WS_NEED_MOST:
+            _ws_need.clear()
         need = _ws_need[key] = int(size())
     if not need:
         return None, 0, None

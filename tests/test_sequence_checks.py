@@ -295,3 +295,17 @@ def test_argument_types_cover_every_entry_point(lib):
     for name in ("vrwkv_decay_attn_fwd", "vrwkv_decay_attn_bwd", "vrwkv_decay_attn_step", "vrwkv_layer_norm_fwd",
                  "vrwkv_layer_norm_bwd"):
         assert getattr(lib, name).argtypes is not None and getattr(lib, name).restype is ctypes.c_int
+
+
+def test_remembered_workspace_sizes_are_bounded(monkeypatch):
+    """A program whose sequences are of ever new lengths does not grow by them."""
+    monkeypatch.setattr(vk, "_ws_need", {})
+    asked = []
+    for n in range(3 * vk._WS_NEED_MOST):
+        def size():
+            asked.append(n)
+            return 0
+        for _ in range(2):
+            assert vk._workspace((1, n), size, None, DEV, None) == (None, 0, None)
+    assert len(vk._ws_need) <= vk._WS_NEED_MOST
+    assert asked == list(range(3 * vk._WS_NEED_MOST))  # once each while it is remembered
