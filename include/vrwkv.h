@@ -469,7 +469,7 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  *            bfloat16 heads above 32 channels of no multiple of 8, copies of
  *            the tensors.  Its contents need no preparation.  Calls that may
  *            run at the same time need separate workspaces.
- * Limits: D <= 128 (UNSUPPORTED above).
+ * Limits: D <= 128, T <= 2^30 (UNSUPPORTED above).
  * Arithmetic: sums, decays and states in float32, products on the tensor
  *   cores from operands split into parts; outputs rounded once.
  *   float32    what the parts leave out is below 2^-21 of a product.
@@ -502,8 +502,8 @@ size_t vrwkv_decay_attn_workspace_bytes(int B, int T, int H, int D,
  *              itself (updated in place).
  * Errors: INVALID_ARG for sizes <= 0, NULL or misaligned pointers, row strides
  *   below H*D, a missing or small workspace, or an output (or the workspace)
- *   that overlaps an input or another output; UNSUPPORTED beyond the limits
- *   or for B*T or H*D >= 2^31.
+ *   that overlaps an input or another output; UNSUPPORTED beyond the limits,
+ *   for B*T or H*D >= 2^31, or for B*H above 2^29 / 3 (the CTAs of a launch).
  */
 vrwkv_status vrwkv_decay_attn_fwd(const void* q, const void* k, const void* v,
                                   long long ldq, long long ldk, long long ldv,
@@ -548,7 +548,7 @@ vrwkv_status vrwkv_decay_attn_bwd(const void* q, const void* k, const void* v,
  *            16 of the device error word (vrwkv_device_status).
  *   out      (B, H*D) dense.
  * Errors: as vrwkv_decay_attn_fwd, plus INVALID_ARG for N <= 0, or N < B
- *   without slots.
+ *   without slots, and UNSUPPORTED for H > 65535.
  */
 vrwkv_status vrwkv_decay_attn_step(const void* q, const void* k, const void* v,
                                    long long ldq, long long ldk, long long ldv,
@@ -567,7 +567,7 @@ vrwkv_status vrwkv_decay_attn_step(const void* q, const void* k, const void* v,
  *   mean, rstd  float32[rows] outputs for the backward pass, or both NULL.
  * Errors: INVALID_ARG for sizes <= 0, NULL or misaligned pointers, a negative
  *   eps, mean without rstd, or an output that overlaps an input or another
- *   output; UNSUPPORTED for rows >= 2^31.
+ *   output; UNSUPPORTED for rows >= 2^31 or C > 2^30.
  */
 vrwkv_status vrwkv_layer_norm_fwd(const void* x, const float* gamma,
                                   const float* beta, float eps, void* y,

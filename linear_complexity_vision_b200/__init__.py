@@ -540,7 +540,14 @@ def _tokens_of(name, t, dims: int):
         raise ValueError(f"{name} must be a ({'B, T, C' if dims == 3 else 'B, C'}) tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    _require_int32(name, max(shape))
     return shape, dtype, device, _dtype_code_of(dtype)
+
+
+def _require_int32(name, n) -> None:
+    """Sizes are passed as C ints, which ctypes would cut off."""
+    if n > 0x7fffffff:
+        raise ValueError(f"{name}: a size of {n} is not below 2^31")
 
 
 def _dtype_code_of(dtype) -> int:
@@ -723,6 +730,7 @@ def decay_attn_step(q, k, v, w, heads: int, state, slots=None, scale: float = 1.
     if len(pool) != 4:
         raise ValueError("state must be a (N, heads, D, D) tensor")
     N = pool[0]
+    _require_int32("state", N)
     _require_f32("state", state, (N, heads, D, D), dev)
     if slots is not None:
         _require_ints("slots", slots, B, dev)
@@ -748,6 +756,7 @@ def _norm_rows(x):
     n = x.numel()
     if len(shape) < 1 or n == 0:
         raise ValueError("x must be a (..., C) tensor with rows")
+    _require_int32("x", shape[-1])
     return shape, n // shape[-1], shape[-1], x.dtype, x.device, _dtype_code_of(x.dtype)
 
 

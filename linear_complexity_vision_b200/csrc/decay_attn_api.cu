@@ -19,6 +19,7 @@ using namespace vrwkv;
 using namespace vrwkv::api;
 
 constexpr int kMaxD = 128;
+constexpr int kMaxT = 1 << 30;  // a segment's end stays an int
 constexpr int kSegUnit = 128;  // segments are multiples of this many tokens
 
 struct Span {
@@ -37,6 +38,7 @@ vrwkv_status check_sizes(int B, int T, int H, int D, vrwkv_dtype dtype) {
     if (B <= 0 || T <= 0 || H <= 0 || D <= 0)
         return fail(VRWKV_ERR_INVALID_ARG, "B, T, H and D must be positive (got %d, %d, %d, %d)", B, T, H, D);
     if (D > kMaxD) return fail(VRWKV_ERR_UNSUPPORTED, "head size D = %d exceeds %d", D, kMaxD);
+    if (T > kMaxT) return fail(VRWKV_ERR_UNSUPPORTED, "T = %d exceeds 2^30", T);
     if ((long long)B * T > INT_MAX || (long long)H * D > INT_MAX)
         return fail(VRWKV_ERR_UNSUPPORTED, "B*T and H*D must be below 2^31");
     return ok();
@@ -388,7 +390,7 @@ bool vec_ok(const void* p, long long ld, int es) { return aligned(p, 4 * es) && 
 extern "C" {
 
 size_t vrwkv_decay_attn_workspace_bytes(int B, int T, int H, int D, vrwkv_dtype dtype, int backward) {
-    if (B <= 0 || T <= 0 || H <= 0 || D <= 0 || D > kMaxD || (dtype != VRWKV_F32 && dtype != VRWKV_BF16)) return 0;
+    if (B <= 0 || T <= 0 || T > kMaxT || H <= 0 || D <= 0 || D > kMaxD || (dtype != VRWKV_F32 && dtype != VRWKV_BF16)) return 0;
     return ws_bytes(B, T, H, D, dtype, backward != 0);
 }
 

@@ -38,6 +38,7 @@ namespace {
 using namespace vrwkv;
 using namespace vrwkv::api;
 
+constexpr int kLnMaxC = 1 << 30;  // a lane's steps of 32 channels stay an int
 constexpr int kLnBwdMaxC = 8192;
 
 // Geometry of the backward pass: a warp per row (vpl vectors a lane) or, with
@@ -107,6 +108,7 @@ vrwkv_status check_ln(long long rows, int C, vrwkv_dtype dtype) {
         return fail(VRWKV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
     if (rows <= 0 || C <= 0)
         return fail(VRWKV_ERR_INVALID_ARG, "rows and C must be positive (got %lld, %d)", rows, C);
+    if (C > kLnMaxC) return fail(VRWKV_ERR_UNSUPPORTED, "C = %d exceeds 2^30", C);
     if (rows > 0x7fffffffLL) return fail(VRWKV_ERR_UNSUPPORTED, "rows must be below 2^31");
     return ok();
 }

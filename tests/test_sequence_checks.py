@@ -309,3 +309,36 @@ def test_remembered_workspace_sizes_are_bounded(monkeypatch):
             assert vk._workspace((1, n), size, None, DEV, None) == (None, 0, None)
     assert len(vk._ws_need) <= vk._WS_NEED_MOST
     assert asked == list(range(3 * vk._WS_NEED_MOST))  # once each while it is remembered
+
+
+@pytest.mark.parametrize("T", [(1 << 30) + 1, (1 << 31) - 1])
+def test_longest_sequences(lib, T):
+    """Beyond 2^30 tokens the end of a segment, rounded up, would not be an int."""
+    for fn, names, ok in ((lib.vrwkv_decay_attn_fwd, FWD, FWD_OK), (lib.vrwkv_decay_attn_bwd, BWD, BWD_OK)):
+        assert _call(fn, names, ok, dict(B=1, T=T)) == 2
+        assert "2^30" in lib.vrwkv_last_error().decode()
+    assert lib.vrwkv_decay_attn_workspace_bytes(1, T, 1, 1, 1, 0) == 0
+
+
+@pytest.mark.parametrize("C", [(1 << 30) + 1, (1 << 31) - 1])
+def test_widest_rows(lib, C):
+    """Beyond 2^30 channels a lane's next one, 32 on, might not be an int."""
+    assert _call(lib.vrwkv_layer_norm_fwd, LNF, LNF_OK, dict(rows=1, C=C)) == 2
+    assert "2^30" in lib.vrwkv_last_error().decode()
+
+
+def test_sizes_that_are_no_c_int_are_refused():
+    """ctypes cuts a C int off without a word: 2^32 + 5 tokens would be 5."""
+    for n in (1 << 31, (1 << 32) + 5):
+        x = FakeCuda((1, n, 4))
+        with pytest.raises(ValueError, match="2\\^31"):
+            vk.decay_attn_fwd(x, x, x, f32(1), 1)
+        with pytest.raises(ValueError, match="2\\^31"):
+            vk.decay_attn_bwd(x, x, x, f32(1), 1, x)
+        row = FakeCuda((1, 4))
+        with pytest.raises(ValueError, match="2\\^31"):
+            vk.decay_attn_step(row, row, row, f32(1), 1, f32(n, 1, 4, 4))
+        with pytest.raises(ValueError, match="2\\^31"):
+            vk.layer_norm_fwd(FakeCuda((1, n)), f32(n), f32(n))
+        with pytest.raises(ValueError, match="2\\^31"):
+            vk.layer_norm_bwd(FakeCuda((1, n)), f32(n), f32(1), f32(1), FakeCuda((1, n)))
