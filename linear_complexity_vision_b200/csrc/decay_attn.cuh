@@ -67,7 +67,9 @@ __device__ __forceinline__ int seg_count(int n, int seg, int seg_tokens) {
 }
 
 // e^{-w n} as 2^{n c}, c = -w log2 e held as a float pair: the exponent is
-// rounded once, so the relative error of the power stays below |w n| 2^-24.
+// rounded once, so the relative error of the power stays below |w n| 2^-24 plus
+// exp2f's own 2 units in the last place (2^-22).  Above 2^24 tokens n is rounded
+// too: |w n| 2^-23.
 struct DecayBase {
     float hi, lo;
 };

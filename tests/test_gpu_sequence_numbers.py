@@ -2,7 +2,10 @@
 infinities and values at the ends of the range go.
 
 Against the float64 oracle, with the names of test_gpu_sequence.py: u = 2^-24,
-n operations, A the sum of the absolute values of a result's terms.
+n operations, A the sum of the absolute values of a result's terms.  A power of a
+decay is off by |w n| u, its exponent's rounding, and exp2f's 2 units, 4 u; a term
+has three powers at most, whose 12 u are within the 16 operations that a count
+has to spare beside its sums.
 """
 import numpy as np
 import pytest
@@ -222,3 +225,16 @@ def test_wait_limits_do_not_count_the_pass_before(vk):  # noqa: F811
             assert all(torch.equal(a, b) for a, b in zip(want, got))
     finally:
         vk.set_wait_limit(2.0)
+
+
+def test_a_decay(vk):  # noqa: F811
+    """The single token's decay alone: a state of ones and a key of zeros.  A power,
+    (|w| + 4) u, and the rounding of the product, u."""
+    import torch
+    H, D = 400, 8
+    w, wd = _dev(np.concatenate([np.exp(np.linspace(-20, 4, H - 3)), [0.0, -0.5, -3.0]]))
+    state = torch.ones(1, H, D, D, device="cuda")
+    x = torch.zeros(1, H * D, device="cuda")
+    vk.decay_attn_step(x, x, x, w, H, state)
+    want = np.exp(-wd)[None, :, None, None]
+    assert (np.abs(_np(state) - want) <= (np.abs(wd)[None, :, None, None] + 5) * U * 1.001 * want).all()
