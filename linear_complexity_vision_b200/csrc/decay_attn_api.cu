@@ -75,14 +75,14 @@ int padded_d(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 // measured alone on an SM, in us for a unit of 128 tokens (and how much of
 // that each further CTA on the same SM adds):
 //                         outputs          states only      CTAs of an SM
-//   tcgen05, D <= 64      1.75             2.0 (+ 0.5)      1 (persistent), 2
+//   tcgen05, D <= 64      2.15             2.0 (+ 0.5)      1 (persistent), 2
 //            D <= 128     4.2              3.0              1
 //            float32      6.5              4.5              1
 //   any size, DP = 32     9 (+ 0.6)        4 (+ 0.6)        3
 //             DP = 64     23 (+ 0.6)       9 (+ 0.6)        3
 //             DP = 128    45               18               1
 // Both sides measured: B = 1, T = 4096, 16 heads of 64, bfloat16: one segment
-// 56 us, eight 32 us; B = 8: one segment 62 us, two 130 us.
+// 69 us, eight 24 us; B = 3: one 70, three 54; B = 8: one 73 us, two 120 us.
 struct Cut {
     int seg_tokens, nseg;
 };
@@ -104,7 +104,7 @@ double pass_us(long long ctas, int units, const PassCost& c) {
 }
 
 Cut plan(int B, int T, int H, int D, vrwkv_dtype dtype, int nprob, bool tc) {
-    static const PassCost kOut[6] = {{1.75, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}, {6.5, 0, 1}};
+    static const PassCost kOut[6] = {{2.15, 0, 1}, {4.2, 0, 1}, {9, 0.6, 3}, {23, 0.6, 3}, {45, 0, 1}, {6.5, 0, 1}};
     static const PassCost kState[6] = {{2.0, 0.5, 2}, {3.0, 0, 1}, {4, 0.6, 3}, {9, 0.6, 3}, {18, 0, 1}, {4.5, 0, 1}};
     const int kind = tc ? (dtype == VRWKV_F32 ? 5 : D <= 64 ? 0 : 1) : (D <= 32 ? 2 : D <= 64 ? 3 : 4);
     const int units = (T + kSegUnit - 1) / kSegUnit;
@@ -131,16 +131,16 @@ Cut plan(int B, int T, int H, int D, vrwkv_dtype dtype, int nprob, bool tc) {
 // to 128 channels, float32 ones of 33 to 64, and work on 128 tokens however few
 // there are; the kernel for any size works on 32.  Both measured, us, forward
 // (tcgen05 : any size), for 8, 160 and 1024 heads:
-//   bfloat16, D = 64   T = 16  5.6 : 5.6    7.5 : 6.0    16.7 : 15.8
-//                      T = 32  5.7 : 6.8    7.5 : 7.3    16.6 : 20.5
-//                      T = 128 6.0 : 25     7.3 : 28     16.9 : 88
-//             D = 32   T = 32  5.6 : 4.2    7.4 : 4.5    16.6 : 11.7
-//                      T = 64  5.8 : 6.8    6.9 : 7.6    16.6 : 21.7
-//             D = 128  T = 8   5.8 : 6.1    10.4 : 10.6  31.8 : 36.8
-//   float32,  D = 64   T = 64  10.3 : 11.5  19.7 : 13.5  71.6 : 42.8
-//                      T = 96  10.8 : 17.1  20.9 : 20.6  77.3 : 68.8
-//                      T = 128 11.3 : 22.7  21.6 : 27.6  79.8 : 94.2
-//             D = 32   T = 128 10.7 : 10.4  20.3 : 12.7  72.8 : 40.2
+//   bfloat16, D = 64   T = 16  5.6 : 5.8    8.3 : 6.2    19.1 : 16.1
+//                      T = 32  5.8 : 6.8    8.3 : 7.6    19.2 : 20.8
+//                      T = 128 6.0 : 25     8.9 : 28     20.4 : 93
+//             D = 32   T = 32  5.9 : 4.4    8.3 : 4.8    19.1 : 12.4
+//                      T = 64  5.8 : 7.2    8.4 : 8.1    19.4 : 22.3
+//             D = 128  T = 8   5.9 : 6.3    11.0 : 11.1  35.9 : 37.8
+//   float32,  D = 64   T = 64  10.2 : 11.5  19.1 : 14.1  67.0 : 43.9
+//                      T = 96  11.0 : 17.2  20.5 : 21.0  78.0 : 70.0
+//                      T = 128 11.6 : 22.6  21.7 : 28.2  83.4 : 95.4
+//             D = 32   T = 128 10.7 : 10.8  20.1 : 13.1  70.9 : 41.2
 // VRWKV_DECAY_TC=0 keeps them on the kernel for any size (diagnostics and tests).
 bool tc_sizes(int T, int D, vrwkv_dtype dtype) {
     if (dtype == VRWKV_F32) return D % 4 == 0 && D > 32 && D <= 64 && T > 96;
@@ -156,11 +156,11 @@ size_t state_floats(int B, int H, int D, int nseg) { return (size_t)B * H * nseg
 // bfloat16 heads that are spread to whole 16-byte vectors first (decay_pack.cuh):
 // how wide, or 0.  Measured, us, forward (spread : as they are), for 8, 160 and
 // 1024 heads:
-//   D = 27  T = 200  13.7 : 25.3  33.7 : 28.1  111 : 78
-//   D = 45  T = 64   11.0 : 14.2  17.8 : 16.6  49.8 : 48.8
-//           T = 96   11.1 : 21.2  20.5 : 24.6  64.5 : 74.8
-//   D = 89  T = 32   12.0 : 8.9   19.7 : 16.1  63.2 : 55.5
-//           T = 48   12.0 : 17.7  20.8 : 33.1  76.3 : 117
+//   D = 27  T = 200  13.7 : 25.6  35.7 : 27.5  118 : 78
+//   D = 45  T = 64   11.1 : 15.7  19.2 : 17.0  53.1 : 49.8
+//           T = 96   11.4 : 23.9  22.3 : 26.3  68.4 : 76.4
+//   D = 89  T = 32   12.0 : 8.9   20.2 : 16.4  67.6 : 56.0
+//           T = 48   12.1 : 18.2  21.4 : 34.4  81.0 : 119
 // (float32, D = 45, T = 200: 23.1 : 41.7, 60.8 : 50.7, 240 : 172, as they are.)
 int spread_width(int T, int D, vrwkv_dtype dtype) {
     return dtype == VRWKV_BF16 && D > 32 && D % 8 != 0 && T > (D <= 64 ? 64 : 32) ? (D + 7) / 8 * 8 : 0;
