@@ -472,7 +472,7 @@ vrwkv_status vrwkv_channel_mix(const void* x, void* out, int B, int T, int C,
  * Limits: D <= 128, T <= 2^30 (UNSUPPORTED above).
  * Arithmetic: sums, decays and states in float32, products on the tensor
  *   cores from operands split into parts; outputs rounded once.
- *   float32    what the parts leave out is below 2^-21 of a product.
+ *   float32    what the parts leave out is below 2^-20 of a product.
  *   bfloat16   q, k, v (gy) as they are; a state that meets q, the decayed
  *              products q.k and the decayed keys that meet v in two bfloat16
  *              parts (2^-17); a state that leaves the call formed from three

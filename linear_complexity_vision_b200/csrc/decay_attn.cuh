@@ -133,20 +133,25 @@ struct Cfg {
 };
 
 // A float32 operand as tf32 values, of which the tensor core reads the upper 19
-// bits: hi, then lo, the remainder.  Cutting bits off a value times 1 + 2^-11
-// leaves it off by at most 2^-11 of itself either way, so hi + lo is off by 2^-22.
-// Float multiplications, since they keep a NaN (the GPU's own has all bits set:
-// adding to them wraps it to 0), and towards zero, since a finite value then
-// stays finite.  What an infinity leaves is NaN.
+// bits: hi, then lo, the remainder.  Before bits are cut off a value is multiplied,
+// which adds half a step of them: to hi 0.72 * 2^-11 of it, half a step on average
+// over a binade, so that lo leans to neither side (the product of two remainders is
+// left out; with 2^-11 it is 5e-8 of a product, always the same way); to lo 2^-11.
+// hi is off by at most 2^-10.6, lo by 2^-11 of itself: a product of two operands by
+// 2^-20.  Multiplications, since they keep a NaN (the GPU's own has all bits set:
+// adding to them wraps it to 0), and towards zero, since a finite value then stays
+// finite.  What an infinity leaves is NaN.
+// Measured, outputs of 2 x 200, heads of 128, against 64 bits: 2.85e-7 of the norm;
+// half steps added to the bits, at the same time, 2.80e-7.  To nearest by the
+// exponent's power of two, 2.80e-7: 21 x 256, 12 heads of 128 194 us in place of 176.
 template <bool EXACT>
 __device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) {
-    constexpr float kHalfStep = 1.00048828125f;
     if (EXACT) {
         hi = __float_as_uint(x);
         lo = 0u;
     } else {
-        hi = __float_as_uint(__fmul_rz(x, kHalfStep)) & 0xffffe000u;
-        lo = __float_as_uint((x - __uint_as_float(hi)) * kHalfStep);
+        hi = __float_as_uint(__fmul_rz(x, 1.0003515625f)) & 0xffffe000u;
+        lo = __float_as_uint((x - __uint_as_float(hi)) * 1.00048828125f);
     }
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

@@ -153,7 +153,7 @@ def test_states_and_decays_that_are_not_finite(vk, dt, D, T, bits):  # noqa: F81
 @pytest.mark.parametrize("D,T", [(9, 100), (64, 64), (128, 200)])
 def test_largest_float32_values(vk, D, T):  # noqa: F811
     """Values up to the type's largest, in v, where the state and the result are far
-    below it.  Parts: 3 * 2^-22 of a product of float32 values, twice in a row."""
+    below it.  The parts leave out 2^-20 of a product, twice in a row."""
     p = Problem("f32", 1, T, 1, D, 37, state=False, w=3.0, scale=2.0 ** -60)
     p.v[0, ::3, ::2] = float(np.finfo(np.float32).max)
     p.vd = _np(p.v)
@@ -238,3 +238,49 @@ def test_a_decay(vk):  # noqa: F811
     vk.decay_attn_step(x, x, x, w, H, state)
     want = np.exp(-wd)[None, :, None, None]
     assert (np.abs(_np(state) - want) <= (np.abs(wd)[None, :, None, None] + 5) * U * 1.001 * want).all()
+
+
+FIRST_CALLS = """
+import torch
+import linear_complexity_vision_b200 as vk
+
+torch.manual_seed(41)
+H, D = 2, {D}
+q, k, v, g = (torch.randn(2, {T}, H * D, device="cuda", dtype=torch.{dtype}) for _ in range(4))
+w, gamma = torch.full((H,), 0.1, device="cuda"), torch.ones(H * D, device="cuda")
+pool = torch.zeros(2, H, D, D, device="cuda")
+
+
+def run():
+    out, last = vk.decay_attn_fwd(q, k, v, w, H)
+    grads = vk.decay_attn_bwd(q, k, v, w, H, g)[:3]
+    y, mean, rstd = vk.layer_norm_fwd(out, gamma, gamma)
+    pool.zero_()
+    one = vk.decay_attn_step(q[:, 0], k[:, 0], v[:, 0], w, H, pool)
+    return [out, last, *grads, y, mean, rstd, *vk.layer_norm_bwd(out, gamma, mean, rstd, g), one, pool]
+
+
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    captured = run()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in captured]
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+vk.device_status()
+print("replayed")
+"""
+
+
+@pytest.mark.parametrize("dtype,D,T", [("bfloat16", 64, 1500), ("float32", 64, 1500), ("bfloat16", 90, 300), ("float32", 20, 40)])
+def test_first_calls_may_be_captured(vk, dtype, D, T):  # noqa: F811
+    """A process whose very first calls are captured: what the library looks up
+    once must not need the stream."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(D=D, T=T, dtype=dtype)], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stderr[-2000:]
