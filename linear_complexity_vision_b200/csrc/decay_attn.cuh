@@ -106,8 +106,8 @@ __device__ __forceinline__ float4 ld4(const char* p) {
 // Why not the FP32 pipes: fed from shared memory with 8 products an operand
 // they measured a quarter of their rate (float32 B=8 T=1024 16 heads of 64:
 // 223 us), while a fragment of m16n8k8 serves 16 products and more (183 us).
-// Bound by those instructions: float32 21 x 256, 12 heads of 128, takes 196 us,
-// half of the 489 products a clock and SM that tf32 measures here.  bfloat16
+// Bound by those instructions: float32 21 x 256, 12 heads of 128, takes 176 us, a
+// little over half of the 489 products a clock and SM that tf32 measures here.  bfloat16
 // heads of an odd width also load by element: 3 x 7518, 15 heads of 89: 1.75 ms.
 //
 // Warps: the token tiles of 16 rows (2), times 2 (DP = 128: 4) parts of the v

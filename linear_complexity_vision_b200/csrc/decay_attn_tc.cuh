@@ -42,8 +42,8 @@
 // sequences) D = 64 runs here too: 8 warps, 98 KB, two CTAs per SM.  Its outputs
 // have a kernel of their own (decay_attn_tc64.cuh).
 //
-// Measured: B = 1, T = 16384, 8 heads of 128, with a final state: 72.5 us (states
-// 30, chain 4, outputs 38; floor 20.7, its bytes).  128 CTAs walk 8 chunks each;
+// Measured: B = 1, T = 16384, 8 heads of 128, with a final state: 73 us (states
+// 30, chain 4, outputs 43; floor 20.7, its bytes).  128 CTAs walk 8 chunks each;
 // the tensor pipe is busy a third of that time and DRAM less: what is left is
 // the chain A -> P -> O -> next chunk of one CTA, whose steps wait for one another.
 // Two chunks at a time, as heads of 64 run them, do not fit: 224 KB of tiles.

@@ -8,12 +8,12 @@
 // serial: four warps keep it in registers, add each chunk's U in turn and hand
 // the operands of O = q X to the stream whose chunk is next.
 //
-// Measured: forward 8 x 4096, 16 heads: 62.5 us (floor 41.0: its bytes), one
-// chunk 1.75 us of an SM; 128 of 148 SMs work, since one head's chunks are
-// serial and a cut would form the states first (two segments: 130 us).
-// Backward, three problems of it: 8 x 4096, 16 heads 171 us (floor 71.8), 64 x
-// 196, 12 heads 62 us (20.6).  Issue slots are 42 to 48 % busy, the tensor pipe
-// 24 to 30 %: bound by the latency of a chunk's steps, of which two overlap; a
+// Measured: forward 8 x 4096, 16 heads: 73 us (floor 41.0: its bytes), one
+// chunk 2.15 us of an SM; 128 of 148 SMs work, since one head's chunks are
+// serial and a cut would form the states first (two segments: 120 us).
+// Backward, three problems of it: 8 x 4096, 16 heads 210 us (floor 71.8), 64 x
+// 196, 12 heads 68 us (20.6).  Issue slots are 45 % busy, the tensor pipe 28 to
+// 36 %: bound by the latency of a chunk's steps, of which two overlap; a
 // third stream has no tensor memory left.  One chunk at a time, in the manner
 // of decay_attn_tc.cuh with two CTAs an SM: 8 x 4096 100 us.
 //

@@ -34,8 +34,8 @@
 // 168 KB of shared memory, all of tensor memory, one CTA per SM.  Bounded waits
 // as in decay_attn_tc.cuh.
 //
-// Measured: 32 x 196 ragged, 6 heads: 33.5 us (floor 4.7: its bytes); backward 3
-// x 1001, 6 heads, eight segments: 50.2 us (3.7); the kernel for any size takes
+// Measured: 32 x 196 ragged, 6 heads: 32.9 us (floor 4.7: its bytes); backward 3
+// x 1001, 6 heads, eight segments: 49.2 us (3.7); the kernel for any size takes
 // 52 and 62 us.  A chunk takes 6.3 us, a CTA of one chunk 10 us.  The working
 // warps are busy 5.5 us of a chunk: splitting q, k and v 2.4 with their loads
 // from L2, P 1.4, X and the output 0.8; the products, fed from shared memory,

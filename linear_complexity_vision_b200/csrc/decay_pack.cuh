@@ -4,7 +4,7 @@
 // there afterwards; the tcgen05 kernels see heads of W.  Element by element on
 // the narrow side, a warp four heads' rows at a time, two channels a lane: bound
 // by those loads' and stores' number.  Measured at 3 x 7518, 15 heads of 89, the
-// whole forward call: 360 us, as they are 1.74 ms (floor 37).
+// whole forward call: 369 us, as they are 1.74 ms (floor 37).
 #pragma once
 
 #include "common.cuh"

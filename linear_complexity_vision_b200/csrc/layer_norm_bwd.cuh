@@ -5,12 +5,13 @@
 // channels a lane go to a warp each (layer_norm_bwd_warp_kernel): a row's two
 // sums then cost 10 shuffles and no barrier, and the next row is on its way in
 // registers while one is worked on.  Measured in a graph, both kernels of the
-// call: 32768 x 1024 bfloat16 44.3 us, 12544 x 768 bfloat16 19.6, 6272 x 384
-// float32 10.1, 32768 x 1024 float32 73.1 us (5.5 TB/s).  The same with the rows
+// call: 32768 x 1024 bfloat16 45.3 us, 12544 x 768 bfloat16 20.2, 6272 x 384
+// float32 10.6, 32768 x 1024 float32 72.4 us (5.6 TB/s).  The same with the rows
 // on their way in a ring of shared memory (bulk copies, four CTAs an SM): 46.7,
 // 21.2, 11.0 and 78.9; with three CTAs and spills for wide float32 rows 126 us.
-// bfloat16 is bound by its arithmetic beside the bytes: each element is unpacked
-// twice and takes eight FP32 operations, paired.  Wider rows, or rows that are
+// bfloat16 rows of 1024 are bound by latency: 163 registers leave three warps a
+// scheduler, which wait for shared memory (gamma) and the sums' shuffles more than
+// for DRAM (1.5 and 0.3 of an instruction's stalls), issue 47 %.  Wider rows, or rows that are
 // not made of aligned 16-byte vectors, go to a CTA each.  Either way a thread
 // keeps the same channels of every row it visits, so their ggamma and gbeta stay
 // in its registers; each CTA leaves one partial row of them, and
